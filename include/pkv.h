@@ -33,6 +33,14 @@
  *   slot = page * page_size + offset; the width is head_dim for K and
  *   head_dim_v for V (pkv_config). Elements are bf16, or FP8 E4M3FN bytes
  *   with one fp32 scale per pool (value = code * scale).
+ * - 4-bit pools (PKV_KV_FP4_E2M1) hold E2M1 codes with one E4M3FN scale for
+ *   every 16 columns of a row and one fp32 scale per pool: value = code *
+ *   block scale * pool scale. They are made of tiles, one for every 16
+ *   consecutive slots and KV head: tile (slot / 16) * num_kv_heads + head, of
+ *   16 * (width / 2 + width / 16) bytes (1152 for width 128): first 16 rows of
+ *   width / 2 code bytes (row slot % 16; column 2i in the low nibble of byte
+ *   i, column 2i + 1 in the high one), then 16 rows of width / 16 scale bytes.
+ *   A tile is one contiguous run, so a KV head's 16 slots are one bulk copy.
  * - Queries are bf16 [tokens][num_q_heads][head_dim], outputs bf16
  *   [tokens][num_q_heads][head_dim_v]; LSE is fp32 [tokens][num_q_heads], the
  *   natural log of sum_j exp(sm_scale * q . k_j).
@@ -70,9 +78,10 @@ extern "C" {
 #define PKV_DEV_BAD_LENGTH 1   /* seq_len < 0, qo_len < 0, qo_len > seq_len, or ceil(seq_len / page_size) > page_table_stride */
 #define PKV_DEV_BAD_PAGE 2     /* page id outside [0, num_pages) */
 #define PKV_DEV_CAPACITY 3     /* total pages / query rows beyond the configured capacity */
-#define PKV_DEV_BAD_SLOT 4     /* set_kv_buffer loc outside [0, num_pages * page_size) */
+#define PKV_DEV_BAD_SLOT 4     /* set_kv_buffer / get_kv_buffer loc outside [0, num_pages * page_size) */
 #define PKV_DEV_QO_TOO_LONG 5  /* decode path: qo_len beyond config.max_qo_len */
 #define PKV_DEV_TREE_TOO_LONG 6 /* draft-tree mask set and a request has more than 64 new tokens */
+#define PKV_DEV_BAD_POSITION 7 /* pkv_rope_set_kv_buffer: position outside [0, max_positions) */
 #define PKV_DEV_TIMEOUT 16     /* a wait inside a kernel ran past the wait limit (pkv_set_wait_limit); the
                                   CTA that waited gave up its remaining work, so the outputs are incomplete */
 
@@ -93,7 +102,7 @@ typedef enum { PKV_SPEC_PREFILL = 0, PKV_SPEC_DECODE = 1 } pkv_spec_mode;
 
 typedef enum { PKV_PATH_INVALID = -1, PKV_PATH_DECODE = 0, PKV_PATH_EXTEND = 1 } pkv_path;
 
-typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1 } pkv_kv_dtype;
+typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1, PKV_KV_FP4_E2M1 = 2 } pkv_kv_dtype;
 
 /* ---- configuration --------------------------------------------------------
  * Fixed for the life of a context; every capacity bounds a fixed-size
@@ -105,9 +114,9 @@ typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1 } pkv_kv_dtype;
  * 16-token page of the configs the library is tuned on, and the 128-token page
  * that the same page, section "The obvious fix, and why it fails", names as
  * fa4's native page size); num_q_heads a multiple of num_kv_heads with a group
- * size num_q_heads / num_kv_heads of at most 16; E4M3 (FP8) pools with head_dim
- * 128 (and V heads of 128) on both paths (other widths with an E4M3 pool
- * return PKV_ERR_UNSUPPORTED). */
+ * size num_q_heads / num_kv_heads of at most 16; E4M3 (FP8) and 4-bit pools
+ * with head_dim 128 (and V heads of 128) on both paths (other widths with such
+ * a pool return PKV_ERR_UNSUPPORTED). */
 typedef struct {
   int32_t num_q_heads;
   int32_t num_kv_heads;
@@ -132,7 +141,9 @@ const char* pkv_status_string(int status);
 int pkv_workspace_bytes(const pkv_config* cfg, size_t* bytes_out);
 
 /* Bytes of the K pool of one layer: num_pages * page_size * num_kv_heads *
- * head_dim * element size. The V pool takes the same with head_dim_v in place
+ * head_dim * element size (4-bit pools: head_dim / 2 + head_dim / 16 bytes in
+ * place of head_dim * element size; UNSUPPORTED unless the slots and head_dim
+ * are multiples of 16). The V pool takes the same with head_dim_v in place
  * of head_dim (the same bytes when the widths are equal). */
 int pkv_pool_bytes(const pkv_config* cfg, size_t* bytes_out);
 
@@ -184,11 +195,67 @@ int pkv_get_metadata(pkv_ctx* ctx, const int32_t** kv_indptr, const int32_t** kv
  * [n_tokens][num_kv_heads][head_dim_v]; d_loc: int32 slots.
  * bf16 pools receive the same bits; E4M3 pools receive
  * e4m3_rn_satfinite(float(x) * inv_scale) (one fp32 multiply, round to nearest
- * even, finite values beyond +-448 saturate). Slots outside the pool are
+ * even, finite values beyond +-448 saturate). 4-bit pools: for every 16
+ * columns y = float(x) * inv_scale, the block scale is
+ * S = e4m3_rn_satfinite(max|y| * fp32(1/6)) and each code is
+ * e2m1_rn_satfinite(y * fp32(1/S)) (all codes 0 where S is 0; infinities
+ * saturate, a NaN makes its block's scale NaN). Slots outside the pool are
  * skipped and recorded as PKV_DEV_BAD_SLOT. Duplicate slots: unspecified
- * winner. Pointers must be 16-byte aligned. */
+ * winner (for 4-bit pools codes and scale may then be of different tokens).
+ * Pointers must be 16-byte aligned. */
 int pkv_set_kv_buffer(pkv_ctx* ctx, void* d_k_pool, void* d_v_pool, const int32_t* d_loc, const void* d_k,
                       const void* d_v, int32_t n_tokens, float k_inv_scale, float v_inv_scale, void* stream);
+
+/* Rotary position embedding of a context's heads: row p of d_cos_sin (device
+ * fp32 [max_positions][rotary_dim], 16-byte aligned) holds cos of position p's
+ * rotary_dim / 2 angles, then their sin. Columns rotary_offset ..
+ * rotary_offset + rotary_dim - 1 of each Q and K head are rotated, the others
+ * pass unchanged. With f = rotary_offset and angle j, the rotated pair is
+ *   interleaved == 0: columns f + j and f + j + rotary_dim / 2,
+ *   interleaved != 0: columns f + 2j and f + 2j + 1,
+ * and (a, b) becomes (a cos - b sin, b cos + a sin), each product and sum
+ * rounded to fp32 once. rotary_dim: a positive multiple of 16; rotary_offset:
+ * a multiple of 8; their sum at most head_dim. */
+typedef struct {
+  const float* d_cos_sin;
+  int32_t max_positions;
+  int32_t rotary_dim;
+  int32_t rotary_offset;
+  int32_t interleaved;
+} pkv_rope;
+
+/* Rotate q and k by their positions and append k and v to the pools, in one
+ * launch. For token i < n_tokens with position d_positions[i]:
+ *   d_q_out[i, h, :]     = bf16(rotated q[i, h, :])
+ *   k_pool[d_loc[i], h]  = rotated k[i, h, :], rounded to the pool's type from
+ *                          fp32 as pkv_set_kv_buffer rounds (bf16 pools: to
+ *                          nearest even)
+ *   v_pool[d_loc[i], h]  = v[i, h, :] as pkv_set_kv_buffer stores it.
+ * d_q, d_k, d_v: bf16 rows of [heads][width], token i at i * stride elements
+ * (q_stride, k_stride, v_stride: multiples of 8, at least heads * width), so
+ * the three may be slices of one projection's rows. d_q_out: bf16 [n_tokens]
+ * [num_q_heads][head_dim], contiguous as the forwards want it, not overlapping
+ * the inputs. d_q and d_q_out may both be NULL: only k and v are stored.
+ * A position outside the table records PKV_DEV_BAD_POSITION and nothing of
+ * its token is written; a slot outside the pool records PKV_DEV_BAD_SLOT and
+ * only the token's K and V are skipped. Duplicate slots: as pkv_set_kv_buffer.
+ * Errors: INVALID_ARG (null or misaligned pointers, strides, overlap, rotary
+ * fields; inverse scales that are not positive and finite with E4M3 or 4-bit
+ * pools), UNSUPPORTED (more than 2^31 - 1 thread blocks), CUDA. */
+int pkv_rope_set_kv_buffer(pkv_ctx* ctx, const pkv_rope* rope, void* d_k_pool, void* d_v_pool, const int32_t* d_loc,
+                           const int32_t* d_positions, const void* d_q, int64_t q_stride, const void* d_k,
+                           int64_t k_stride, const void* d_v, int64_t v_stride, void* d_q_out, int32_t n_tokens,
+                           float k_inv_scale, float v_inv_scale, void* stream);
+
+/* The way back: rows of the pools as bf16,
+ *   d_k[i, h, :] = bf16(value of k_pool[d_loc[i], h, :])   for i < n_tokens,
+ * d_v alike (value = code times block scale, exact, then one fp32 multiply by
+ * k_scale / v_scale, then one rounding; bf16 pools: the same bits, scales
+ * ignored). d_k, d_v: bf16 [n_tokens][num_kv_heads][width], 16-byte aligned.
+ * Slots outside the pool are recorded as PKV_DEV_BAD_SLOT and their rows left
+ * as they were. Slots may repeat. Errors as the forwards' scales. */
+int pkv_get_kv_buffer(pkv_ctx* ctx, const void* d_k_pool, const void* d_v_pool, const int32_t* d_loc, void* d_k,
+                      void* d_v, int32_t n_tokens, float k_scale, float v_scale, void* stream);
 
 /* forward_decode: attention of every query row against its request's paged
  * keys, using the metadata of the last pkv_build_metadata. Split-KV: each
@@ -198,9 +265,10 @@ int pkv_set_kv_buffer(pkv_ctx* ctx, void* d_k_pool, void* d_v_pool, const int32_
  * d_q: bf16 [T][num_q_heads][head_dim] (T = sum of qo_len), d_out: bf16
  * [T][num_q_heads][head_dim_v] (scores contract head_dim columns, the output
  * has the V heads' width), d_lse: fp32 [T][num_q_heads] or NULL. k_scale / v_scale multiply
- * E4M3 codes (ignored for bf16 pools). Pointers must be 16-byte aligned.
+ * E4M3 codes, or 4-bit codes times their block scales (ignored for bf16
+ * pools). Pointers must be 16-byte aligned.
  * sm_scale must be positive and finite, and so must k_scale and v_scale with
- * an E4M3 pool (INVALID_ARG otherwise). Verify batches follow the draft-tree
+ * an E4M3 or 4-bit pool (INVALID_ARG otherwise). Verify batches follow the draft-tree
  * mask when one is set (pkv_set_tree_mask).
  * Errors: INVALID_ARG, UNSUPPORTED (group size with max_qo_len beyond one
  * 128-row tile), CUDA. */
@@ -213,7 +281,8 @@ int pkv_forward_decode(pkv_ctx* ctx, const void* d_q, const void* d_k_pool, cons
  * E4M3 pool the kernel widens each tile's codes to f16 in shared memory
  * (exact) and runs its MMAs in f16, Q and P rounded to f16, k_scale folded
  * into the score scale and v_scale into the output, as the decode path does;
- * the workspace holds no copy of the pool. */
+ * the workspace holds no copy of the pool. 4-bit pools likewise, a code times
+ * its block scale being exact in f16. */
 int pkv_forward_extend(pkv_ctx* ctx, const void* d_q, const void* d_k_pool, const void* d_v_pool, float sm_scale,
                        float k_scale, float v_scale, void* d_out, float* d_lse, void* stream);
 
@@ -259,6 +328,25 @@ int pkv_set_tree_mask(pkv_ctx* ctx, const uint64_t* d_tree_mask);
  * alive while forwards that use it run; a captured graph replays with
  * whatever it then holds. */
 int pkv_set_attention_sinks(pkv_ctx* ctx, const float* d_sinks);
+
+/* Cap of the scores: with cap > 0 every score s_j = sm_scale * q . k_j becomes
+ *   cap * tanh(s_j / cap)
+ * before the bias below, the masks, the softmax and the sinks. 0 (the default)
+ * turns it off. Applies to every forward of the context until set again; a
+ * captured graph keeps the value of its capture. Errors: INVALID_ARG (negative,
+ * infinite or NaN). */
+int pkv_set_logit_cap(pkv_ctx* ctx, float cap);
+
+/* Bias by distance: with slopes set (device fp32 [num_q_heads]), head h's score
+ * of the query row at position i for the key at position j gains
+ *   slopes[h] * (j - i),   i = seq_len - qo_len + the row's index,
+ * after the cap. Slopes must be finite; a positive one favours near keys.
+ * Applies to every forward of the context until set again; NULL (the default)
+ * turns it off. The caller owns the buffer and keeps it alive while forwards
+ * that use it run; a captured graph replays with whatever it then holds.
+ * Drafts of a tree have no single distance to their ancestors' slots, so a
+ * forward with slopes and an active tree mask returns PKV_ERR_UNSUPPORTED. */
+int pkv_set_alibi_slopes(pkv_ctx* ctx, const float* d_slopes);
 
 /* Bound on every wait inside the kernels (a warp waiting for a tile, a
  * result or a free buffer), in nanoseconds; 0 restores the default of 2 s.

@@ -41,6 +41,7 @@ _LIB_PATH = os.path.join(_BUILD_DIR, "libpkv_oracle.so")
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
+KV_F64 = 2  # pools of decoded values (float64), see fp4_unpack
 
 MODE_EXTEND, MODE_DECODE, MODE_IDLE, MODE_TARGET_VERIFY, MODE_DRAFT_EXTEND = 0, 1, 2, 3, 4
 SPEC_PREFILL, SPEC_DECODE = 0, 1
@@ -89,7 +90,7 @@ def _load():
         lib.oracle_lse_merge.argtypes = [ctypes.c_int, ctypes.c_int, vp, vp, vp, vp]
         lib.oracle_attention.restype = ctypes.c_int
         lib.oracle_attention.argtypes = [ctypes.c_int] * 7 + [vp, vp, vp, i32p, i32p, i32p, i32p, vp, vp,
-                                                               ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                                               ctypes.c_double, vp, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                                                ctypes.c_int64, i32p, i32p, vp, vp, ctypes.c_int]
         lib.oracle_pool_bytes.restype = ctypes.c_int64
         lib.oracle_pool_bytes.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
@@ -174,6 +175,85 @@ def set_kv_buffer(k_pool, v_pool, loc, k_new, v_new, kv_dtype=KV_BF16, k_inv_sca
                              float(k_inv_scale), float(v_inv_scale))
 
 
+# ---------------------------------------------------------------- 4-bit pools
+# A pool is made of tiles, one per 16 slots and KV head: 16 rows of D/2 bytes
+# (even column in the low nibble), then 16 rows of D/16 E4M3 block scales.
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def e2m1_decode_array(codes) -> np.ndarray:
+    codes = np.asarray(codes, dtype=np.uint8)
+    return np.where(codes & 8, -1.0, 1.0) * E2M1[codes & 7]
+
+
+def e2m1_encode_array(x) -> np.ndarray:
+    """Nearest code of finite or infinite values, ties to the even code, beyond 6 saturating."""
+    x = np.asarray(x, dtype=np.float64)
+    a = np.minimum(np.abs(x), 6.0)
+    far = np.abs(a[..., None] - E2M1)
+    near = far == far.min(-1, keepdims=True)
+    even = near & (np.arange(8) % 2 == 0)
+    code = np.where(even.any(-1), even.argmax(-1), near.argmax(-1)).astype(np.uint8)
+    return code | (np.signbit(x).astype(np.uint8) << 3)
+
+
+def fp4_encode_rows(rows, inv_scale):
+    """fp32 rows [..., D] -> (codes [..., D], block scale bytes [..., D/16]) by the definition: y = x * inv_scale and
+    z = y * fp32(1 / S) in single fp32 roundings, S = e4m3(max|y| * fp32(1/6)); a NaN makes its block's S NaN."""
+    rows = np.asarray(rows, dtype=np.float32)
+    with np.errstate(all="ignore"):
+        y = (rows * np.float32(inv_scale)).astype(np.float32)
+        b = y.reshape(*y.shape[:-1], -1, 16)
+        a = np.abs(b).max(-1)  # keeps a NaN
+        s8 = np.array([e4m3_encode(float(v)) for v in (a * np.float32(1.0 / 6.0)).astype(np.float32).ravel()],
+                      dtype=np.uint8).reshape(a.shape)
+        s = e4m3_decode_array(s8).astype(np.float32)
+        r = np.where(s > 0, np.float32(1.0) / s, np.float32(0.0)).astype(np.float32)
+        z = (b * r[..., None]).astype(np.float32)
+        codes = e2m1_encode_array(np.where(np.isnan(z), 0.0, z))
+    return codes.reshape(rows.shape), s8
+
+
+def _fp4_views(pool, num_kv_heads, width):
+    tiles = pool.reshape(-1, num_kv_heads, 16 * (width // 2 + width // 16))
+    return (tiles[..., :8 * width].reshape(-1, num_kv_heads, 16, width // 2),
+            tiles[..., 8 * width:].reshape(-1, num_kv_heads, 16, width // 16))
+
+
+def fp4_store(pool, num_kv_heads, loc, codes, scales):
+    """Codes [n, Hkv, D] and scales [n, Hkv, D/16] into slots loc of a pool's bytes, in place."""
+    rows, sc = _fp4_views(pool, num_kv_heads, codes.shape[-1])
+    for i, slot in enumerate(np.asarray(loc)):
+        rows[slot // 16, :, slot % 16] = codes[i, :, 0::2] | (codes[i, :, 1::2] << 4)
+        sc[slot // 16, :, slot % 16] = scales[i]
+
+
+def fp4_unpack(pool, num_kv_heads, width) -> np.ndarray:
+    """Values code * block scale, float64 [slots, Hkv, D]."""
+    rows, sc = _fp4_views(np.asarray(pool), num_kv_heads, width)
+    codes = np.stack([rows & 15, rows >> 4], -1).reshape(*rows.shape[:-1], width)
+    values = e2m1_decode_array(codes) * np.repeat(e4m3_decode_array(sc), 16, axis=-1)
+    return np.ascontiguousarray(values.swapaxes(1, 2).reshape(-1, num_kv_heads, width))
+
+
+# ---------------------------------------------------------------- rotation
+def rotate(x, positions, cos_sin, rotary_offset=0, interleaved=False, dtype=np.float32):
+    """Rows [n, heads, D] (fp32 values) with their rotary columns turned by the positions' angles; dtype float32: each
+    product and sum rounded once, as the operator is defined; float64: the formula."""
+    x = np.asarray(x, dtype=np.float32).astype(dtype)
+    R = cos_sin.shape[1]
+    row = np.asarray(cos_sin, dtype=np.float32)[np.asarray(positions)].astype(dtype)
+    c, s = row[:, None, :R // 2], row[:, None, R // 2:]
+    j = np.arange(R // 2)
+    ia, ib = (2 * j, 2 * j + 1) if interleaved else (j, j + R // 2)
+    a, b = x[..., rotary_offset + ia], x[..., rotary_offset + ib]
+    y = x.copy()
+    with np.errstate(all="ignore"):
+        y[..., rotary_offset + ia] = (a * c).astype(dtype) - (b * s).astype(dtype)
+        y[..., rotary_offset + ib] = (b * c).astype(dtype) + (a * s).astype(dtype)
+    return y
+
+
 def lse_merge(o_parts, lse_parts):
     lib = _load()
     o_parts = np.ascontiguousarray(o_parts, dtype=np.float64)
@@ -186,7 +266,7 @@ def lse_merge(o_parts, lse_parts):
 
 
 def attention(q, k_pool, v_pool, meta, num_q_heads, num_kv_heads, page_size, sm_scale, kv_dtype=KV_BF16,
-              k_scale=1.0, v_scale=1.0, rows=None, nthreads=None, tree_mask=None, sinks=None):
+              k_scale=1.0, v_scale=1.0, rows=None, nthreads=None, tree_mask=None, sinks=None, logit_cap=0.0, slopes=None):
     """fp64 attention over the paged pool.
 
     q: uint16 bf16 bits [T, Hq, D]; pools: uint16 / uint8, K [slots, Hkv, D]
@@ -197,7 +277,10 @@ def attention(q, k_pool, v_pool, meta, num_q_heads, num_kv_heads, page_size, sm_
     bottom-right causal) or uint64 [T]: bit j of token t's word lets it see
     the j-th new token of its request (every cached key stays visible).
     sinks: None or float [Hq], each head's sink logit (a key with that score
-    and a zero value vector).
+    and a zero value vector). logit_cap: 0, or c of c * tanh(score / c).
+    slopes: None or float [Hq], each head's bias by distance, slope * (key
+    position - query position), after the cap. Pools of kv_dtype KV_F64 hold
+    decoded values.
     """
     lib = _load()
     q = np.ascontiguousarray(q, dtype=np.uint16)
@@ -230,9 +313,13 @@ def attention(q, k_pool, v_pool, meta, num_q_heads, num_kv_heads, page_size, sm_
     sk = None if sinks is None else np.ascontiguousarray(sinks, dtype=np.float64)
     if sk is not None:
         assert sk.shape == (hq,)
+    sl = None if slopes is None else np.ascontiguousarray(slopes, dtype=np.float64)
+    if sl is not None:
+        assert sl.shape == (hq,)
     st = lib.oracle_attention(bs, hq, num_kv_heads, d, dv, page_size, int(kv_dtype), _ptr(q), _ptr(k_pool),
                               _ptr(v_pool), kvp_p, kvi_p, last_p, qoi_p, None if tm is None else _ptr(tm),
-                              None if sk is None else _ptr(sk),
+                              None if sk is None else _ptr(sk), float(logit_cap),
+                              None if sl is None else _ptr(sl),
                               float(sm_scale), float(k_scale),
                               float(v_scale), n_rows, rt_p, rh_p, _ptr(out_o), _ptr(out_lse), int(nthreads))
     if st != 0:

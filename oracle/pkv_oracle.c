@@ -50,6 +50,7 @@
 /* KV pool element encodings */
 #define ORACLE_KV_BF16 0
 #define ORACLE_KV_FP8_E4M3 1
+#define ORACLE_KV_F64 2 /* values already decoded (4-bit pools, whose tiles are unpacked by the caller) */
 
 /* ForwardMode values and the two speculative attention modes. */
 #define ORACLE_MODE_EXTEND 0
@@ -129,6 +130,7 @@ uint8_t oracle_e4m3_encode(float xf) {
 
 static double kv_value(const void* pool, int kv_dtype, int64_t elem, double scale) {
   if (kv_dtype == ORACLE_KV_BF16) return oracle_bf16_decode(((const uint16_t*)pool)[elem]) * scale;
+  if (kv_dtype == ORACLE_KV_F64) return ((const double*)pool)[elem] * scale;
   return oracle_e4m3_decode(((const uint8_t*)pool)[elem]) * scale;
 }
 
@@ -256,6 +258,8 @@ typedef struct {
   const int32_t* qo_indptr;
   const uint64_t* tree_mask; /* NULL: chain drafts (bottom-right causal) */
   const double* sinks;       /* NULL, or one sink logit per query head */
+  double logit_cap;          /* 0, or the cap c of the scores: c * tanh(s / c) */
+  const double* slopes;      /* NULL, or one distance slope per query head: s + slope * (key - query position) */
   double sm_scale, k_scale, v_scale;
   int64_t n_rows; /* number of (token, q-head) rows to compute */
   const int32_t* row_token; /* NULL: every row in token-major order */
@@ -332,6 +336,8 @@ static int attention_row(const attn_job* j, int t, int h, double* scores, double
     double dot = 0.0;
     for (int d = 0; d < D; ++d) dot += qd[d] * kv_value(j->k_pool, j->kv_dtype, base + d, j->k_scale);
     scores[p] = j->sm_scale * dot;
+    if (j->logit_cap > 0) scores[p] = j->logit_cap * tanh(scores[p] / j->logit_cap);
+    if (j->slopes) scores[p] += j->slopes[h] * (double)(p - limit);
     if (scores[p] > m) m = scores[p];
   }
   if (sink > m) m = sink;
@@ -389,12 +395,13 @@ int oracle_attention(int bs, int num_q_heads, int num_kv_heads, int head_dim, in
                      int kv_dtype,
                      const uint16_t* q, const void* k_pool, const void* v_pool, const int32_t* kv_indptr,
                      const int32_t* kv_indices, const int32_t* kv_last_page_len, const int32_t* qo_indptr,
-                     const uint64_t* tree_mask, const double* sinks, double sm_scale, double k_scale, double v_scale, int64_t n_rows, const int32_t* row_token,
+                     const uint64_t* tree_mask, const double* sinks, double logit_cap, const double* slopes,
+                     double sm_scale, double k_scale, double v_scale, int64_t n_rows, const int32_t* row_token,
                      const int32_t* row_head, double* out_o, double* out_lse, int nthreads) {
   if (bs < 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || head_dim <= 0 || head_dim_v <= 0 ||
       page_size <= 0)
     return ORACLE_ERR_ARG;
-  if (kv_dtype != ORACLE_KV_BF16 && kv_dtype != ORACLE_KV_FP8_E4M3) return ORACLE_ERR_ARG;
+  if (kv_dtype != ORACLE_KV_BF16 && kv_dtype != ORACLE_KV_FP8_E4M3 && kv_dtype != ORACLE_KV_F64) return ORACLE_ERR_ARG;
   if (nthreads < 1) nthreads = 1;
   attn_job job;
   memset(&job, 0, sizeof job);
@@ -414,6 +421,8 @@ int oracle_attention(int bs, int num_q_heads, int num_kv_heads, int head_dim, in
   job.qo_indptr = qo_indptr;
   job.tree_mask = tree_mask;
   job.sinks = sinks;
+  job.logit_cap = logit_cap;
+  job.slopes = slopes;
   job.sm_scale = sm_scale;
   job.k_scale = k_scale;
   job.v_scale = v_scale;

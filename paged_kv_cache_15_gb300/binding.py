@@ -20,19 +20,20 @@ LIB_PATH = os.path.join(_HERE, "_build", "libpkv.so")
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CAPACITY, PKV_ERR_CUDA, PKV_ERR_DEVICE = range(6)
 (PKV_DEV_OK, PKV_DEV_BAD_LENGTH, PKV_DEV_BAD_PAGE, PKV_DEV_CAPACITY, PKV_DEV_BAD_SLOT, PKV_DEV_QO_TOO_LONG,
- PKV_DEV_TREE_TOO_LONG) = range(7)
+ PKV_DEV_TREE_TOO_LONG, PKV_DEV_BAD_POSITION) = range(8)
 PKV_DEV_TIMEOUT = 16
 PKV_MODE_EXTEND, PKV_MODE_DECODE, PKV_MODE_IDLE, PKV_MODE_TARGET_VERIFY, PKV_MODE_DRAFT_EXTEND = range(5)
 PKV_SPEC_PREFILL, PKV_SPEC_DECODE = 0, 1
 PKV_PATH_INVALID, PKV_PATH_DECODE, PKV_PATH_EXTEND = -1, 0, 1
-PKV_KV_BF16, PKV_KV_FP8_E4M3 = 0, 1
+PKV_KV_BF16, PKV_KV_FP8_E4M3, PKV_KV_FP4_E2M1 = 0, 1, 2
 
 # every function the header declares (checked against include/pkv.h by the tests)
 EXPORTS = ("pkv_status_string", "pkv_workspace_bytes", "pkv_pool_bytes", "pkv_create", "pkv_destroy",
            "pkv_select_backend", "pkv_build_metadata", "pkv_get_metadata", "pkv_set_kv_buffer",
            "pkv_forward_decode", "pkv_forward_extend", "pkv_forward", "pkv_get_device_error", "pkv_describe",
            "pkv_forward_decode_static", "pkv_set_tree_mask", "pkv_set_attention_sinks", "pkv_set_wait_limit",
-           "pkv_test_hold_first_load")
+           "pkv_test_hold_first_load", "pkv_rope_set_kv_buffer", "pkv_get_kv_buffer", "pkv_set_logit_cap",
+           "pkv_set_alibi_slopes")
 
 
 class PkvError(RuntimeError):
@@ -45,6 +46,11 @@ class pkv_config(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int32) for name in (
         "num_q_heads", "num_kv_heads", "head_dim", "page_size", "kv_dtype", "num_pages", "max_batch",
         "max_pages_total", "max_q_tokens", "max_qo_len", "head_dim_v")]
+
+
+class pkv_rope(ctypes.Structure):
+    _fields_ = [("d_cos_sin", ctypes.c_void_p)] + [(name, ctypes.c_int32) for name in (
+        "max_positions", "rotary_dim", "rotary_offset", "interleaved")]
 
 
 _lock = threading.Lock()
@@ -80,6 +86,12 @@ def lib():
                                                   vp, vp, vp]),
             "pkv_forward": (ctypes.c_int, [vp, ctypes.c_int, ctypes.c_int, vp, vp, vp, ctypes.c_float,
                                            ctypes.c_float, ctypes.c_float, vp, vp, vp]),
+            "pkv_rope_set_kv_buffer": (ctypes.c_int, [vp, ctypes.POINTER(pkv_rope), vp, vp, vp, vp, vp, ctypes.c_int64,
+                                                      vp, ctypes.c_int64, vp, ctypes.c_int64, vp, i32, ctypes.c_float,
+                                                      ctypes.c_float, vp]),
+            "pkv_get_kv_buffer": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, i32, ctypes.c_float, ctypes.c_float, vp]),
+            "pkv_set_logit_cap": (ctypes.c_int, [vp, ctypes.c_float]),
+            "pkv_set_alibi_slopes": (ctypes.c_int, [vp, vp]),
             "pkv_set_tree_mask": (ctypes.c_int, [vp, vp]),
             "pkv_set_attention_sinks": (ctypes.c_int, [vp, vp]),
             "pkv_set_wait_limit": (ctypes.c_int, [vp, ctypes.c_uint32, vp]),
@@ -110,6 +122,27 @@ def _ptr(t: Optional[torch.Tensor]):
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t: Optional[torch.Tensor], what: str):
+    """Device pointer and token stride (elements) of bf16 rows [tokens, heads, width], whose tokens may lie apart
+    (slices of a fused projection) but whose own columns are contiguous."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dim() != 3 or t.dtype != torch.bfloat16:
+        raise ValueError(f"{what}: expected bf16 [tokens, heads, width]")
+    if t.shape[0] and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{what}: expected each token's heads and columns to be contiguous")
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def _int32(t: torch.Tensor, what: str):
+    if t.dtype != torch.int32:
+        raise ValueError(f"{what}: expected int32")
+    return _ptr(t)
 
 
 def _stream(stream=None):
@@ -175,6 +208,37 @@ def pkv_set_kv_buffer(ctx, k_pool, v_pool, loc, k, v, k_inv_scale=1.0, v_inv_sca
            "pkv_set_kv_buffer")
 
 
+def pkv_rope_set_kv_buffer(ctx, k_pool, v_pool, loc, positions, cos_sin, q, k, v, q_out, rotary_offset=0,
+                           interleaved=False, k_inv_scale=1.0, v_inv_scale=1.0, stream=None) -> None:
+    """Rotate q and k by their positions and append k and v to the pools. q, k, v: bf16 [tokens, heads, width], views
+    with a token stride of their own allowed; cos_sin: fp32 [max_positions, rotary_dim], the cosines of each
+    position's angles and then their sines; q_out: contiguous (q and q_out None: k and v alone)."""
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+        raise ValueError("cos_sin: expected fp32 [max_positions, rotary_dim]")
+    n = int(loc.shape[0])
+    if positions.shape[0] != n or any(t is not None and t.shape[0] != n for t in (q, k, v, q_out)):
+        raise ValueError("loc, positions, q, k, v and q_out hold different numbers of tokens")
+    if (q is None) != (q_out is None) or (q is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype)):
+        raise ValueError("q_out: expected a tensor like q")
+    rope = pkv_rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(rotary_offset), int(bool(interleaved)))
+    _ptr(cos_sin)
+    (qp, qs), (kp, ks), (vp_, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    _check(lib().pkv_rope_set_kv_buffer(ctx, ctypes.byref(rope), _ptr(k_pool), _ptr(v_pool), _int32(loc, "loc"),
+                                        _int32(positions, "positions"), qp, qs, kp, ks, vp_, vs, _ptr(q_out), n,
+                                        float(k_inv_scale), float(v_inv_scale), _stream(stream)),
+           "pkv_rope_set_kv_buffer")
+
+
+def pkv_get_kv_buffer(ctx, k_pool, v_pool, loc, k, v, k_scale=1.0, v_scale=1.0, stream=None) -> None:
+    """Rows of the pools at slots loc, as bf16, into k and v ([tokens, num_kv_heads, width], contiguous)."""
+    n = int(loc.shape[0])
+    for t in (k, v):
+        if t.dtype != torch.bfloat16 or t.shape[0] != n:
+            raise ValueError("k and v: expected bf16 with loc's number of tokens")
+    _check(lib().pkv_get_kv_buffer(ctx, _ptr(k_pool), _ptr(v_pool), _int32(loc, "loc"), _ptr(k), _ptr(v), n,
+                                   float(k_scale), float(v_scale), _stream(stream)), "pkv_get_kv_buffer")
+
+
 def pkv_forward_decode(ctx, q, k_pool, v_pool, sm_scale, out, lse=None, k_scale=1.0, v_scale=1.0,
                        stream=None) -> None:
     _check(lib().pkv_forward_decode(ctx, _ptr(q), _ptr(k_pool), _ptr(v_pool), float(sm_scale), float(k_scale),
@@ -204,6 +268,19 @@ def pkv_set_attention_sinks(ctx, sinks) -> None:
     """Per-query-head sink logits (fp32 device tensor [num_q_heads]) for the
     forwards that follow, or None to turn sinks off."""
     _check(lib().pkv_set_attention_sinks(ctx, _ptr(sinks)), "pkv_set_attention_sinks")
+
+
+def pkv_set_logit_cap(ctx, cap: float) -> None:
+    """Cap the scores of the forwards that follow: cap * tanh(score / cap); 0 turns it off."""
+    _check(lib().pkv_set_logit_cap(ctx, float(cap)), "pkv_set_logit_cap")
+
+
+def pkv_set_alibi_slopes(ctx, slopes) -> None:
+    """Per-query-head slopes (fp32 device tensor [num_q_heads]) of a bias by distance, slope * (key position - query
+    position), for the forwards that follow, or None to turn it off."""
+    if slopes is not None and slopes.dtype != torch.float32:
+        raise ValueError("slopes: expected fp32")
+    _check(lib().pkv_set_alibi_slopes(ctx, _ptr(slopes)), "pkv_set_alibi_slopes")
 
 
 def pkv_set_wait_limit(ctx, limit_ns: int, stream=None) -> None:

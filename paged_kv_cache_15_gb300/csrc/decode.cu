@@ -38,6 +38,7 @@
 // memory before use, and every other key outside the visible range is masked
 // to -inf, so unused pool slots never reach the result.
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -46,16 +47,16 @@
 namespace pkv {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 // DK: width of the Q and K heads; DV: of the V heads and output rows (equal
 // except for models whose K and V heads differ, 192 / 128).
-template <int DK_, int DV_, bool FP8_, int WK_, int KPW_, int STAGES_, int RT_>
+// KV: the pool's element type (pkv_kv_dtype).
+template <int DK_, int DV_, int KV_, int WK_, int KPW_, int STAGES_, int RT_>
 struct DecodeCfg {
   static constexpr int DK = DK_;
   static constexpr int DV = DV_;
-  static constexpr bool FP8 = FP8_;
+  static constexpr bool FP8 = KV_ == PKV_KV_FP8_E4M3;
+  static constexpr bool FP4 = KV_ == PKV_KV_FP4_E2M1;
+  static constexpr bool F16 = KV_ != PKV_KV_BF16;  // MMAs in f16 (codes widened exactly), else bf16
   // key-major tile: keys along the MMA's M, RT tiles of 8 query rows along N
   static constexpr int RT = RT_;
   static constexpr int WR = 1;    // one row position (the rows are the MMA's N)
@@ -73,17 +74,24 @@ struct DecodeCfg {
   static constexpr int kRowBytesV = DV * kElem;
   static constexpr int kColBlocksK = kRowBytesK / 128;
   static constexpr int kColBlocksV = kRowBytesV / 128;
-  static constexpr int kTileBytesK = kStageKeys * kRowBytesK;  // a stage: K tile, then V tile
-  static constexpr int kTileBytesV = kStageKeys * kRowBytesV;
+  // a stage: K tile, then V tile (4-bit pools: their 16-slot tiles as they lie in the pool)
+  static constexpr int kTileBytesK = FP4 ? kStagePages * fp4_tile_bytes(DK) : kStageKeys * kRowBytesK;
+  static constexpr int kTileBytesV = FP4 ? kStagePages * fp4_tile_bytes(DV) : kStageKeys * kRowBytesV;
   static constexpr int kStageBytes = kTileBytesK + kTileBytesV;
-  static constexpr int kBarOffset = STAGES * kStageBytes;
+  // the key warps combine through scratch of their own (4-bit pools, whose
+  // stages are smaller than the scratch), or through the unit's last stage
+  static constexpr bool kOwnScratch = FP4;
+  static constexpr int kScrRows = kOwnScratch ? 8 * RT_ : 16;
+  static constexpr int kScrOffset = STAGES * kStageBytes;
+  static constexpr int kBarOffset = kScrOffset + (kOwnScratch ? WK * kScrRows * DV * 4 : 0);
   static constexpr int kMlOffset = kBarOffset + 2 * STAGES * 8;
   static constexpr int kAbortOffset = kMlOffset + WK * 16 * 2 * 4;
   static constexpr int kUnitQOffset = kAbortOffset + 16;  // unit queue: 2 full + 2 empty barriers, 2 ids
   static constexpr int kSmemBytes = kUnitQOffset + 40 + 1024;  // + alignment slack
-  static_assert(kRowBytesK % 128 == 0 && kRowBytesV % 128 == 0, "rows must be whole 128-byte swizzle spans");
+  static_assert(FP4 || (kRowBytesK % 128 == 0 && kRowBytesV % 128 == 0), "rows must be whole 128-byte swizzle spans");
+  static_assert(!FP4 || (DK == 128 && DV == 128 && kStagePages <= 16), "4-bit tiles of 128-wide heads, one lane a copy");
   static_assert(KPW % 16 == 0 && kStageKeys % kSegSlots == 0, "stage must hold whole pages");
-  static_assert(!(WK > 1) || (WK * 16 * DV * 4 <= kStageBytes), "merge scratch must fit in one stage");
+  static_assert(kOwnScratch || WK * 16 * DV * 4 <= kStageBytes, "merge scratch must fit in one stage");
   static_assert(WK > 1 && RT >= 1 && RT <= 2, "key-major tiles: one or two 8-row tiles, key warps combined");
 };
 
@@ -97,7 +105,35 @@ struct DecodeArgs {
   float v_scale;     // multiplies the output (E4M3 pools), 1 for bf16
   const uint64_t* tree;  // draft-tree mask word per query token, or null (chain drafts)
   const float* sinks;    // sink logit per query head, or null
+  ScoreMods mods;        // score cap and distance bias (kExtrasScores)
+  const uint8_t *k_pool, *v_pool;  // the pools' bytes (4-bit pools: bulk copies of their tiles)
 };
+
+// 4-bit tiles: MMA key row i of a 16-key block holds key fp4_key(i) of the
+// block, an order in which the row pairs read together by ld.shared lie in
+// different halves of the banks.
+__device__ __forceinline__ int fp4_key(int i) { return i ^ ((i >> 1) & 1); }
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
 
 // Byte offset of (row, 16-byte chunk) inside a swizzled [rows][128 B] column block.
 __device__ __forceinline__ uint32_t swz(int row, int chunk) {
@@ -198,9 +234,10 @@ __device__ __forceinline__ void merge_row(const DecodeArgs& a, long long pbase, 
   if (a.lse && lane == 0) a.lse[orow] = lse;
 }
 
-// EXTRAS: draft-tree mask words or attention sinks are in use (a separate
-// instantiation, so plain batches run without that code).
-template <class C, bool EXTRAS>
+// EXTRAS (enum Extras): draft-tree mask words or attention sinks are in use, or
+// a score cap or bias (instantiations of their own, so plain batches run
+// without that code).
+template <class C, int EXTRAS>
 __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                                                      const __grid_constant__ CUtensorMap tmap_v,
                                                                      DecodeArgs a) {
@@ -218,8 +255,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
   volatile int* s_uq = reinterpret_cast<volatile int*>(uq_empty + 2);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint64_t* const tree_words = EXTRAS ? a.tree : nullptr;
-  const float* const sinks = EXTRAS ? a.sinks : nullptr;
+  const uint64_t* const tree_words = EXTRAS != kExtrasNone ? a.tree : nullptr;
+  const float* const sinks = EXTRAS != kExtrasNone ? a.sinks : nullptr;
   int* plan = a.m.plan;
   pdl_launch_dependents();
 
@@ -237,9 +274,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
   }
   // Stage buffers start as zeros: rows of a partly filled stage are then always
   // finite (zeros or earlier valid keys) and their zero weights stay zero.
-  for (int i = tid; i < C::STAGES * C::kStageBytes / 16; i += C::kThreads)
-    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
+  // (4-bit tiles always come whole, and no other row of theirs is read.)
+  if constexpr (!C::FP4) {
+    for (int i = tid; i < C::STAGES * C::kStageBytes / 16; i += C::kThreads)
+      reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
   __syncthreads();
   // launched with programmatic serialization: the metadata (and the K/V this
   // step stored) are only read after the preceding grid has finished
@@ -247,6 +287,72 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
 
   const int n_units = plan[kDecodeItems] * a.num_kv_heads;
 
+  if (C::FP4 && warp == C::kConsumerWarps) {
+    // ------------------------------------------------------------ producer of 4-bit tiles
+    // The units and their queue are those of the producer below. Each 16-slot
+    // tile of a head is one contiguous run: lane p copies the stage's p-th K
+    // tile, lane 16 + p its p-th V tile, and the next stage's segment indices
+    // are on their way meanwhile.
+    const uint64_t pol = policy_evict_first();
+    const int p = lane & 15;
+    const bool is_v = lane >= 16;
+    const uint8_t* const pool = is_v ? a.v_pool : a.k_pool;
+    int slot = 0;
+    uint32_t phase = 0;
+    uint32_t armed = 0, armed_phase = 0;
+    int w = (int)blockIdx.x < n_units ? (int)blockIdx.x : -1;
+    bool stop = false;
+    const bool hold_first = blockIdx.x == 0 && __ldcg(plan + kHoldLoad) != 0;
+    for (int iu = 0; !stop; ++iu) {
+      const int q = iu & 1;
+      if (!mbar_wait_warp(&uq_empty[q], ((iu >> 1) & 1) ^ 1, plan, s_abort)) {
+        *s_abort = 1;
+        break;
+      }
+      if (lane == 0) {
+        s_uq[q] = w;
+        mbar_arrive(&uq_full[q]);
+      }
+      if (w < 0) break;
+      int claimed = n_units;
+      if (lane == 0 && n_units > (int)gridDim.x) claimed = (int)gridDim.x + atomicAdd(&plan[kDecodeNext], 1);
+      const DecodeItem it = a.m.decode_items[w / a.num_kv_heads];
+      const int g = w % a.num_kv_heads;
+      const int base = a.m.seg_indptr[it.b] + it.p0;
+      const int npages = it.p1 - it.p0;
+      const int nst = (npages + C::kStagePages - 1) / C::kStagePages;
+      int next = p < min(C::kStagePages, npages) ? a.m.seg_indices[base + p] : 0;
+      for (int st = 0; st < nst; ++st) {
+        const int page = next;
+        const int np = min(C::kStagePages, npages - st * C::kStagePages);
+        const int left = npages - (st + 1) * C::kStagePages;
+        next = p < min(C::kStagePages, left) ? a.m.seg_indices[base + (st + 1) * C::kStagePages + p] : 0;
+        if (!mbar_wait_warp(&empty[slot], phase ^ 1, plan, s_abort)) {
+          *s_abort = 1;
+          stop = true;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(np * (fp4_tile_bytes(DK) + fp4_tile_bytes(DV))));
+        __syncwarp();
+        if (p < np && !(hold_first && iu == 0 && st == 0)) {
+          constexpr int kBytes = fp4_tile_bytes(DK);  // (DV == DK)
+          uint8_t* dst = smem + slot * C::kStageBytes + (is_v ? C::kTileBytesK : 0) + p * kBytes;
+          bulk_load_hint(dst, pool + ((long long)page * a.num_kv_heads + g) * kBytes, kBytes, &full[slot], pol);
+        }
+        armed |= 1u << slot;
+        armed_phase = (armed_phase & ~(1u << slot)) | (phase << slot);
+        if (++slot == C::STAGES) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+      claimed = __shfl_sync(0xffffffffu, claimed, 0);
+      w = claimed < n_units ? claimed : -1;
+    }
+    for (int s = 0; s < C::STAGES; ++s)
+      if (armed & (1u << s)) mbar_wait(&full[s], (armed_phase >> s) & 1, plan);
+    return;
+  }
   if (warp == C::kConsumerWarps) {
     // ------------------------------------------------------------ producer (one lane)
     if (lane == 0) {
@@ -383,7 +489,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
         const int rn = 8 * j + g8;
         const bool vn = rn < rows_valid;
         const long long qrow = ((long long)(q0 + rn / G) * a.num_q_heads + g * G + rn % G) * DK;
-        if constexpr (!C::FP8) {
+        if constexpr (C::FP4) {
+          // contraction order of the 4-bit rows: lane t4 holds columns
+          // 32t .. 32t + 31, k-step kk's slots {2t,2t+1} <- D 32t+4kk+{0,1} and
+          // {2t+8,2t+9} <- D 32t+4kk+{2,3}
+#pragma unroll
+          for (int p = 0; p < DK / 32; ++p) {
+            const uint4 x = vn ? *reinterpret_cast<const uint4*>(a.q + qrow + 32 * t4 + 8 * p) : make_uint4(0, 0, 0, 0);
+            qf[2 * p][j][0] = pack_f16(bf16lo(x.x), bf16hi(x.x));
+            qf[2 * p][j][1] = pack_f16(bf16lo(x.y), bf16hi(x.y));
+            qf[2 * p + 1][j][0] = pack_f16(bf16lo(x.z), bf16hi(x.z));
+            qf[2 * p + 1][j][1] = pack_f16(bf16lo(x.w), bf16hi(x.w));
+          }
+        } else if constexpr (!C::FP8) {
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk) {
             const int c0 = kk * 16 + 2 * t4;
@@ -416,6 +534,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
 #pragma unroll
       for (int j = 0; j < RT; ++j) m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.f;
       auto kcol = [&](int mt, int hi) { return C::FP8 ? 16 * mt + 2 * g8 + hi : 16 * mt + 8 * hi + g8; };
+      // key of the 16-key block that this lane's MMA row g8 holds (row g8 + 8: that + 8)
+      const int krow = C::FP4 ? fp4_key(g8) : g8;
+      // distance slopes of this lane's rows, in the log2 domain
+      float slope[RT][2];
+      if constexpr (EXTRAS == kExtrasScores) {
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * j + 2 * t4 + e;
+            slope[j][e] = a.mods.slopes && r < rows_valid ? a.mods.slopes[g * G + r % G] * kLog2e : 0.f;
+          }
+      }
 
       for (int st = 0; st < nst; ++st) {
         // a failed wait keeps this warp on the common control flow (so every
@@ -433,12 +564,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
           const int r0 = L - stage_key0;
           const int r1 = min(C::kStagePages, npages - st * C::kStagePages) * kSegSlots;
           uint8_t* vb8 = smem + slot * C::kStageBytes + C::kTileBytesK;
-          const int n16 = (r1 - r0) * C::kColBlocksV * 8;
-          for (int i = cw * 32 + lane; i < n16; i += C::kConsumerWarps * 32) {
-            const int row = r0 + i / (C::kColBlocksV * 8);
-            const int rest = i % (C::kColBlocksV * 8);
-            const int cb = rest / 8, ch = rest % 8;
-            *reinterpret_cast<uint4*>(vb8 + cb * C::kStageKeys * 128 + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+          if constexpr (C::FP4) {
+            // zero block scales zero the rows (their codes are finite whatever they are)
+            const int i = cw * 32 + lane;
+            if (i < r1 - r0)
+              *reinterpret_cast<uint2*>(vb8 + (r0 / kSegSlots) * fp4_tile_bytes(DV) + kSegSlots * (DV / 2) +
+                                        (r0 % kSegSlots + i) * (DV / 16)) = make_uint2(0, 0);
+          } else {
+            const int n16 = (r1 - r0) * C::kColBlocksV * 8;
+            for (int i = cw * 32 + lane; i < n16; i += C::kConsumerWarps * 32) {
+              const int row = r0 + i / (C::kColBlocksV * 8);
+              const int rest = i % (C::kColBlocksV * 8);
+              const int cb = rest / 8, ch = rest % 8;
+              *reinterpret_cast<uint4*>(vb8 + cb * C::kStageKeys * 128 + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+            }
           }
           fence_proxy_async_smem();
           named_bar_sync(1, C::kConsumerWarps * 32);
@@ -454,7 +593,32 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
             float s[RT][4];
 #pragma unroll
             for (int j = 0; j < RT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-            if constexpr (!C::FP8) {
+            if constexpr (C::FP4) {
+              // lane: 32 codes (two blocks) of key rows g8 and g8 + 8, times
+              // their block scales (exact in f16: at most 6 significant bits)
+              const uint32_t tile = kbase + (kr0 / kSegSlots) * fp4_tile_bytes(DK);
+              uint32_t kf[2][16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int row = krow + 8 * h;
+                const uint4 x = lds_v4(tile + row * (DK / 2) + 16 * t4);
+                const uint32_t sc =
+                    e4m3x2_to_f16x2((uint16_t)lds_u16(tile + kSegSlots * (DK / 2) + row * (DK / 16) + 2 * t4));
+                const uint32_t s0 = __byte_perm(sc, 0, 0x1010), s1 = __byte_perm(sc, 0, 0x3232);
+                e2m1x8_to_f16x2(x.x, kf[h]);
+                e2m1x8_to_f16x2(x.y, kf[h] + 4);
+                e2m1x8_to_f16x2(x.z, kf[h] + 8);
+                e2m1x8_to_f16x2(x.w, kf[h] + 12);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) kf[h][i] = mul_f16x2(kf[h][i], i < 8 ? s0 : s1);
+              }
+#pragma unroll
+              for (int kk = 0; kk < DK / 16; ++kk) {
+                const uint32_t ka[4] = {kf[0][2 * kk], kf[1][2 * kk], kf[0][2 * kk + 1], kf[1][2 * kk + 1]};
+#pragma unroll
+                for (int j = 0; j < RT; ++j) mma_f16(s[j], ka, qf[kk][j][0], qf[kk][j][1]);
+              }
+            } else if constexpr (!C::FP8) {
               const int key = kr0 + (lane & 15);
 #pragma unroll
               for (int kk = 0; kk < DK / 16; ++kk) {
@@ -491,6 +655,17 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
               }
             }
             // ---- mask, online softmax over the 16 keys (log2 domain) ----
+            if constexpr (EXTRAS == kExtrasScores) {
+#pragma unroll
+              for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    s[j][2 * h + e] =
+                        (a.mods.cap2 != 0.f ? capped_score(a.mods, s[j][2 * h + e]) : s[j][2 * h + e] * a.scale_log2) +
+                        slope[j][e] * (float)(abs0 + krow + 8 * h - lim[j][e]);
+            }
             if (tree && abs0 + 15 >= prefix) {
               // the block reaches the drafts: raw scores of drafts outside a
               // row's tree to -inf (the scale below is positive)
@@ -502,7 +677,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
                   const uint64_t tw = r < rows_valid ? tree_words[q0 + r / G] : ~0ull;
 #pragma unroll
                   for (int h = 0; h < 2; ++h) {
-                    const int dj = abs0 + g8 + 8 * h - prefix;
+                    const int dj = abs0 + krow + 8 * h - prefix;
                     if (dj >= 0 && !(dj < 64 && ((tw >> dj) & 1ull))) s[j][2 * h + e] = -INFINITY;
                   }
                 }
@@ -513,11 +688,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
             for (int j = 0; j < RT; ++j) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int kp = abs0 + g8 + 8 * h;
+                const int kp = abs0 + krow + 8 * h;
                 const bool ok = kp < key_end;
+                const float scale = EXTRAS == kExtrasScores ? 1.f : a.scale_log2;
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  s[j][2 * h + e] = (ok && kp <= lim[j][e]) ? s[j][2 * h + e] * a.scale_log2 : -INFINITY;
+                  s[j][2 * h + e] = (ok && kp <= lim[j][e]) ? s[j][2 * h + e] * scale : -INFINITY;
               }
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
@@ -551,11 +727,42 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
             uint32_t pb[RT][2];
 #pragma unroll
             for (int j = 0; j < RT; ++j) {
-              pb[j][0] = movmatrix_trans(C::FP8 ? pack_f16(s[j][0], s[j][1]) : pack_bf16(s[j][0], s[j][1]));
-              pb[j][1] = movmatrix_trans(C::FP8 ? pack_f16(s[j][2], s[j][3]) : pack_bf16(s[j][2], s[j][3]));
+              pb[j][0] = movmatrix_trans(C::F16 ? pack_f16(s[j][0], s[j][1]) : pack_bf16(s[j][0], s[j][1]));
+              pb[j][1] = movmatrix_trans(C::F16 ? pack_f16(s[j][2], s[j][3]) : pack_bf16(s[j][2], s[j][3]));
             }
             // ---- O^T += V^T P^T ----
-            if constexpr (!C::FP8) {
+            if constexpr (C::FP4) {
+              // lane: the 16 codes of block g8 (columns 16g .. 16g + 15) of its
+              // four keys; m-row g8 of m-tile mt is column 16g + 2mt, m-row g8 + 8
+              // the next. Two keys' codes of a column are brought together in one
+              // byte, so a conversion gives the A register's key pair.
+              const uint32_t tile = vbase + (kr0 / kSegSlots) * fp4_tile_bytes(DV);
+              uint32_t vf[2][2][8];  // [key half][column parity][mt]
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int k0 = fp4_key(2 * t4) + 8 * h, k1 = fp4_key(2 * t4 + 1) + 8 * h;
+                const uint2 x = lds_v2(tile + k0 * (DV / 2) + 8 * g8), y = lds_v2(tile + k1 * (DV / 2) + 8 * g8);
+                const uint32_t scales = tile + kSegSlots * (DV / 2) + g8;
+                const uint32_t sc = e4m3x2_to_f16x2(
+                    (uint16_t)(lds_u8(scales + k0 * (DV / 16)) | (lds_u8(scales + k1 * (DV / 16)) << 8)));
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                e2m1x8_to_f16x2((x.x & kLow) | ((y.x << 4) & ~kLow), vf[h][0]);
+                e2m1x8_to_f16x2((x.y & kLow) | ((y.y << 4) & ~kLow), vf[h][0] + 4);
+                e2m1x8_to_f16x2(((x.x >> 4) & kLow) | (y.x & ~kLow), vf[h][1]);
+                e2m1x8_to_f16x2(((x.y >> 4) & kLow) | (y.y & ~kLow), vf[h][1] + 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  vf[h][0][i] = mul_f16x2(vf[h][0][i], sc);
+                  vf[h][1][i] = mul_f16x2(vf[h][1][i], sc);
+                }
+              }
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                const uint32_t va[4] = {vf[0][0][mt], vf[0][1][mt], vf[1][0][mt], vf[1][1][mt]};
+#pragma unroll
+                for (int j = 0; j < RT; ++j) mma_f16(o[mt][j], va, pb[j][0], pb[j][1]);
+              }
+            } else if constexpr (!C::FP8) {
               const int key = kr0 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
@@ -594,7 +801,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
             }
           }
         }
-        const bool hold = st == nst - 1;  // last stage doubles as merge scratch
+        const bool hold = !C::kOwnScratch && st == nst - 1;  // last stage doubles as merge scratch
         if (!hold) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[slot]);
@@ -630,6 +837,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
       };
       // scratch columns XOR-swizzled by row so a store's 32 lanes hit 32 banks
       auto kswz = [](int r) { return ((r >> 1) & 3) << (C::FP8 ? 4 : 3); };
+      // 4-bit pools: column 16b + k of row r lies at 8k + b, both bank bits
+      // above b mixed with k / 4 and with the row, so that neither the stores
+      // (lanes over b and r) nor the loads (lanes over b and k / 4) collide
+      auto scol4 = [&](int b8, int k, int r) { return (8 * k + b8) ^ (((k >> 2) & 3) << 3) ^ kswz(r); };
       if (nst == 0) {
         // empty key range (padding request): zero output, -inf LSE
         if (wk == 0 && !skip) {
@@ -644,9 +855,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
           }
         }
       } else {
-        named_bar_sync(1, C::kConsumerWarps * 32);  // everyone done reading the held stage
-        float* scr = reinterpret_cast<float*>(smem + slot * C::kStageBytes);  // [WK][16][DV]
-        float* my = scr + wk * 16 * DV;
+        // (scratch of its own is free: every warp has passed the loop-top vote
+        // since the last unit's rows were read)
+        if constexpr (!C::kOwnScratch) named_bar_sync(1, C::kConsumerWarps * 32);  // everyone done reading the held stage
+        float* scr = reinterpret_cast<float*>(smem + (C::kOwnScratch ? C::kScrOffset : slot * C::kStageBytes));
+        float* my = scr + wk * C::kScrRows * DV;  // scr: [WK][kScrRows][DV]
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -656,7 +869,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int r = 8 * j + 2 * t4 + e;
-                my[r * DV + (kcol(mt, hi) ^ kswz(r))] = o[mt][j][2 * hi + e];
+                my[r * DV + (C::FP4 ? scol4(g8, 2 * mt + hi, r) : kcol(mt, hi) ^ kswz(r))] = o[mt][j][2 * hi + e];
               }
         if (g8 == 0) {
 #pragma unroll
@@ -674,7 +887,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
         const int ctid = cw * 32 + lane;
         const int nrows = skip ? 0 : min(rows_valid, C::kRows);
         for (int idx = ctid; idx < nrows * (DV / 4); idx += nthr) {
-          const int r = idx / (DV / 4), c4 = idx % (DV / 4);
+          const int r = idx / (DV / 4);
+          // four columns from 4 * c4; 4-bit pools: consecutive threads on consecutive blocks
+          const int sub = idx % (DV / 4);
+          const int c4 = C::FP4 ? 4 * (sub & 7) + (sub >> 3) : sub;
           float mw[C::WK], lw[C::WK];
           float M = -INFINITY;
 #pragma unroll
@@ -693,7 +909,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < C::WK; ++k) {
-            const float4 x = *reinterpret_cast<const float4*>(scr + (k * 16 + r) * DV + ((c4 * 4) ^ kswz(r)));
+            float4 x;
+            if constexpr (C::FP4) {
+              const float* row = scr + (k * C::kScrRows + r) * DV;
+              const int b8 = c4 >> 2, k0 = (c4 & 3) * 4;
+              x = make_float4(row[scol4(b8, k0, r)], row[scol4(b8, k0 + 1, r)], row[scol4(b8, k0 + 2, r)],
+                              row[scol4(b8, k0 + 3, r)]);
+            } else {
+              x = *reinterpret_cast<const float4*>(scr + (k * 16 + r) * DV + ((c4 * 4) ^ kswz(r)));
+            }
             acc.x += x.x * wgt[k];
             acc.y += x.y * wgt[k];
             acc.z += x.z * wgt[k];
@@ -708,12 +932,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
                                                                 pack_bf16(acc.z * inv * fs, acc.w * inv * fs));
           if (c4 == 0 && lrow) *lrow = lse_r;
         }
-        fence_proxy_async_smem();
-        named_bar_sync(1, C::kConsumerWarps * 32);  // scratch reads done before the stage is refilled
-        if (lane == 0) mbar_arrive(&empty[slot]);
-        if (++slot == C::STAGES) {
-          slot = 0;
-          phase ^= 1;
+        if constexpr (!C::kOwnScratch) {
+          fence_proxy_async_smem();
+          named_bar_sync(1, C::kConsumerWarps * 32);  // scratch reads done before the stage is refilled
+          if (lane == 0) mbar_arrive(&empty[slot]);
+          if (++slot == C::STAGES) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
     }
@@ -767,6 +993,8 @@ template <class C>
 int run_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, float sm_scale, float k_scale,
                float v_scale, void* out, float* lse, cudaStream_t st) {
   CUtensorMap tk, tv;
+  memset(&tk, 0, sizeof(tk));
+  memset(&tv, 0, sizeof(tv));
   const CUtensorMapDataType dt = C::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t inner_k = (uint64_t)c.cfg.num_kv_heads * C::DK;
   const uint64_t inner_v = (uint64_t)c.cfg.num_kv_heads * C::DV;
@@ -774,10 +1002,11 @@ int run_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   const uint32_t box_inner = 128 / C::kElem;
   // L2 fills no wider than one head's row of an E4M3 pool (128 bytes)
   const CUtensorMapL2promotion promo = C::FP8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-  if (encode_tmap_2d(&tk, dt, const_cast<void*>(k_pool), inner_k, slots, inner_k * C::kElem, box_inner, kSegSlots,
-                     CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
+  // (4-bit tiles come by untiled bulk copies)
+  if (!C::FP4 && encode_tmap_2d(&tk, dt, const_cast<void*>(k_pool), inner_k, slots, inner_k * C::kElem, box_inner,
+                                kSegSlots, CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
     return PKV_ERR_CUDA;
-  if (encode_tmap_2d(&tv, dt, const_cast<void*>(v_pool), inner_v, slots, inner_v * C::kElem, box_inner, kSegSlots,
+  if (!C::FP4 && encode_tmap_2d(&tv, dt, const_cast<void*>(v_pool), inner_v, slots, inner_v * C::kElem, box_inner, kSegSlots,
                      CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
     return PKV_ERR_CUDA;
   DecodeArgs a;
@@ -788,12 +1017,17 @@ int run_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   a.num_q_heads = c.cfg.num_q_heads;
   a.num_kv_heads = c.cfg.num_kv_heads;
   a.group = c.cfg.num_q_heads / c.cfg.num_kv_heads;
-  const bool fp8 = c.cfg.kv_dtype == PKV_KV_FP8_E4M3;
-  a.scale_log2 = sm_scale * (fp8 ? k_scale : 1.f) * kLog2e;
-  a.v_scale = fp8 ? v_scale : 1.f;
+  const bool scaled = c.cfg.kv_dtype != PKV_KV_BF16;
+  a.scale_log2 = sm_scale * (scaled ? k_scale : 1.f) * kLog2e;
+  a.v_scale = scaled ? v_scale : 1.f;
   a.tree = active_tree(c);
   a.sinks = c.sinks;
-  auto kernel = (a.tree || a.sinks) ? decode_splitkv_kernel<C, true> : decode_splitkv_kernel<C, false>;
+  a.mods = score_mods(c, a.scale_log2);
+  a.k_pool = static_cast<const uint8_t*>(k_pool);
+  a.v_pool = static_cast<const uint8_t*>(v_pool);
+  auto kernel = a.mods.cap2 > 0.f || a.mods.slopes ? decode_splitkv_kernel<C, kExtrasScores>
+                : a.tree || a.sinks                ? decode_splitkv_kernel<C, kExtrasMask>
+                                                   : decode_splitkv_kernel<C, kExtrasNone>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
     return PKV_ERR_CUDA;
   if (launch_pdl(kernel, dim3(c.decode_ctas), dim3(C::kThreads), C::kSmemBytes, st, tk, tv, a) != cudaSuccess)
@@ -804,14 +1038,16 @@ int run_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
 // Tile shapes: one or two 8-row key-major tiles per unit; four key warps
 // split each stage's keys. With 192-wide K heads (bf16) a stage is 40 KB, so
 // two stages keep two CTAs on an SM.
-using DecBf16D128_1 = DecodeCfg<128, 128, false, 4, 16, 3, 1>;
-using DecBf16D128_2 = DecodeCfg<128, 128, false, 4, 16, 3, 2>;
-using DecBf16D64_1 = DecodeCfg<64, 64, false, 4, 16, 4, 1>;
-using DecBf16D64_2 = DecodeCfg<64, 64, false, 4, 16, 4, 2>;
-using DecFp8D128_1 = DecodeCfg<128, 128, true, 4, 32, 3, 1>;
-using DecFp8D128_2 = DecodeCfg<128, 128, true, 4, 32, 3, 2>;
-using DecBf16D192_1 = DecodeCfg<192, 128, false, 4, 16, 2, 1>;
-using DecBf16D192_2 = DecodeCfg<192, 128, false, 4, 16, 2, 2>;
+using DecBf16D128_1 = DecodeCfg<128, 128, PKV_KV_BF16, 4, 16, 3, 1>;
+using DecBf16D128_2 = DecodeCfg<128, 128, PKV_KV_BF16, 4, 16, 3, 2>;
+using DecBf16D64_1 = DecodeCfg<64, 64, PKV_KV_BF16, 4, 16, 4, 1>;
+using DecBf16D64_2 = DecodeCfg<64, 64, PKV_KV_BF16, 4, 16, 4, 2>;
+using DecFp8D128_1 = DecodeCfg<128, 128, PKV_KV_FP8_E4M3, 4, 32, 3, 1>;
+using DecFp8D128_2 = DecodeCfg<128, 128, PKV_KV_FP8_E4M3, 4, 32, 3, 2>;
+using DecBf16D192_1 = DecodeCfg<192, 128, PKV_KV_BF16, 4, 16, 2, 1>;
+using DecBf16D192_2 = DecodeCfg<192, 128, PKV_KV_BF16, 4, 16, 2, 2>;
+using DecFp4D128_1 = DecodeCfg<128, 128, PKV_KV_FP4_E2M1, 4, 32, 4, 1>;
+using DecFp4D128_2 = DecodeCfg<128, 128, PKV_KV_FP4_E2M1, 4, 32, 4, 2>;
 
 
 }  // namespace
@@ -832,12 +1068,12 @@ int decode_row_warps(const pkv_config& cfg) {
 // tiles.
 int decode_stage_pages(const pkv_config& cfg) {
   if (decode_row_warps(cfg) > 1) return kExtendKeys / kSegSlots;
-  return cfg.kv_dtype == PKV_KV_FP8_E4M3 ? 8 : 4;
+  return cfg.kv_dtype != PKV_KV_BF16 ? 8 : 4;
 }
 
 int launch_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, float sm_scale, float k_scale,
                   float v_scale, void* out, float* lse, cudaStream_t st) {
-  const bool fp8 = c.cfg.kv_dtype == PKV_KV_FP8_E4M3;
+  const bool fp8 = c.cfg.kv_dtype == PKV_KV_FP8_E4M3, fp4 = c.cfg.kv_dtype == PKV_KV_FP4_E2M1;
   const int D = c.cfg.head_dim;
   // verify shapes (more than 16 rows per KV head): the tcgen05 tile kernel
   // over this path's plan
@@ -846,6 +1082,11 @@ int launch_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool,
   // decode shapes (at most 16 rows): key-major tiles of one or two 8-row tiles
   const bool rt1 = c.cfg.max_qo_len * (c.cfg.num_q_heads / c.cfg.num_kv_heads) <= 8;
 #define PKV_RUN(CFG) return run_decode<CFG>(c, q, k_pool, v_pool, sm_scale, k_scale, v_scale, out, lse, st)
+  if (fp4 && D == 128) {
+    if (rt1) PKV_RUN(DecFp4D128_1);
+    PKV_RUN(DecFp4D128_2);
+  }
+  if (fp4) return PKV_ERR_UNSUPPORTED;
   if (!fp8 && D == 128) {
     if (rt1) PKV_RUN(DecBf16D128_1);
     PKV_RUN(DecBf16D128_2);
@@ -876,6 +1117,8 @@ int launch_split_merge(Ctx& c, void* out, float* lse, int max_rows_per_head, boo
   a.v_scale = 1.f;
   a.tree = nullptr;
   a.sinks = c.sinks;
+  a.mods = ScoreMods{};  // the merge combines finished partial rows
+  a.k_pool = a.v_pool = nullptr;
   // one warp per (token, head) row, 8 warps per CTA, 3 CTAs per SM
   const long long rows = (long long)c.cfg.max_q_tokens * c.cfg.num_q_heads;
   const long long grid = std::min<long long>((rows + 7) / 8, (long long)c.num_sms * 3);

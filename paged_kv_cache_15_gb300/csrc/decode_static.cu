@@ -71,7 +71,7 @@ extern "C" int pkv_forward_decode_static(const pkv_config* cfg, int32_t batch, c
   if (d_error && (reinterpret_cast<uintptr_t>(d_error) & 3)) return PKV_ERR_INVALID_ARG;
   // masked scores become -inf before the scale multiplies them: it must be positive
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return PKV_ERR_INVALID_ARG;
-  if (cfg->kv_dtype == PKV_KV_FP8_E4M3 &&
+  if (cfg->kv_dtype != PKV_KV_BF16 &&
       (!(k_scale > 0.f) || !std::isfinite(k_scale) || !(v_scale > 0.f) || !std::isfinite(v_scale)))
     return PKV_ERR_INVALID_ARG;
 

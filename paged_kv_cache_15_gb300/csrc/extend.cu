@@ -41,8 +41,6 @@
 namespace pkv {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 // Bounds on one tile's row sum of p = 2^(s * scale - m_ref) between which the
 // reference m_ref stays put (see the softmax role). With bf16 P any p up to
 // 2^16 is representable; with f16 P (E4M3 pools) p stays at most 2^15, below
@@ -201,17 +199,19 @@ __device__ __forceinline__ UnitKV unit_kv(const ExtendTile& u) {
 
 // DK: width of the Q and K heads; DV: of the V heads and the output rows
 // (equal except for models whose K and V heads differ, 192 / 128).
-// FP8: E4M3 pools. TMA brings the codes into raw rings (RK / RV tiles of one
-// byte per code), the K and V producer warps widen them to f16 (exactly) into
-// the operand rings, and the MMAs run in f16 with Q and P rounded to f16.
-template <int DK_, int DV_, int NK_, int NV_, bool FP8_ = false, int RK_ = 0, int RV_ = 0>
+// KV: the pool's element type (pkv_kv_dtype). E4M3 and 4-bit pools: TMA brings
+// the codes into raw rings (RK / RV tiles), the K and V producer warps widen
+// them to f16 (exactly; 4-bit codes times their block scales) into the operand
+// rings, and the MMAs run in f16 with Q and P rounded to f16.
+template <int DK_, int DV_, int NK_, int NV_, int KV_ = PKV_KV_BF16, int RK_ = 0, int RV_ = 0>
 struct ExtCfg {
   static constexpr int DK = DK_;
   static constexpr int DV = DV_;
   static constexpr int NK = NK_;  // K ring depth
   static constexpr int NV = NV_;  // V ring depth
-  static constexpr bool FP8 = FP8_;
-  static constexpr int RK = RK_;  // raw E4M3 K tiles in flight
+  static constexpr bool FP4 = KV_ == PKV_KV_FP4_E2M1;
+  static constexpr bool CODED = KV_ != PKV_KV_BF16;  // E4M3 or 4-bit: f16 operands widened from codes
+  static constexpr int RK = RK_;  // raw K tiles in flight
   static constexpr int RV = RV_;
   static constexpr int kThreads = 352;
   static constexpr int kProducerWarp = 8;   // K tiles
@@ -225,7 +225,8 @@ struct ExtCfg {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = 2 * kQBytes;
   static constexpr int kVOff = kKOff + NK * kTileBytesK;
-  static constexpr int kRawTileBytes = kExtendKeys * 128;  // 128 E4M3 codes per row
+  // 128 E4M3 codes per row, or the pool's 16-slot tiles of 4-bit codes
+  static constexpr int kRawTileBytes = FP4 ? kExtendKeys / kSegSlots * fp4_tile_bytes(DK) : kExtendKeys * 128;
   static constexpr int kRawKOff = kVOff + NV * kTileBytesV;
   static constexpr int kRawVOff = kRawKOff + RK * kRawTileBytes;
   static constexpr int kBarOff = kRawVOff + RV * kRawTileBytes;
@@ -237,8 +238,8 @@ struct ExtCfg {
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert(DV <= 128, "O needs at most 128 TMEM columns per tile");
-  static_assert(!FP8 || (DK == 128 && DV == 128 && RK >= 1 && RV >= 1), "E4M3 rows are one 128-byte span");
-  static_assert(FP8 || (RK == 0 && RV == 0), "raw rings only for E4M3 pools");
+  static_assert(!CODED || (DK == 128 && DV == 128 && RK >= 1 && RV >= 1), "E4M3 rows are one 128-byte span");
+  static_assert(CODED || (RK == 0 && RV == 0), "raw rings only for coded pools");
 };
 
 struct ExtendArgs {
@@ -248,7 +249,7 @@ struct ExtendArgs {
   float* lse;
   int num_q_heads, num_kv_heads, group;
   float scale_log2;
-  float v_scale;     // multiplies the output rows (the V pool's scale of an E4M3 pool; 1 for bf16)
+  float v_scale;     // multiplies the output rows (the V pool's scale of a coded pool; 1 for bf16)
   int q_tma;         // 1 when the group divides 128: a Q tile is one TMA box of 128/G tokens x G heads
   int q_box_tokens;  // 128 / group
   int out_32B;       // out is 32-byte aligned: output rows are written with 32-byte stores
@@ -257,6 +258,8 @@ struct ExtendArgs {
   // 1: the units are the decode plan's (request, split) items, the decode
   // path's verify shapes (at most 128 rows per KV head); 0: the extend plan
   int dplan;
+  ScoreMods mods;  // score cap and distance bias (kExtrasScores)
+  const uint8_t *k_pool, *v_pool;  // the pools' bytes (4-bit pools: bulk copies of their tiles)
 };
 
 // Work unit idx of the plan the kernel runs. A decode-plan item (request b,
@@ -282,9 +285,10 @@ __device__ __forceinline__ ExtendTile load_unit(const ExtendArgs& a, int idx) {
   return u;
 }
 
-// EXTRAS: draft-tree mask words or attention sinks are in use (a separate
-// instantiation, so plain batches run the causal kernel without that code).
-template <class C, bool EXTRAS>
+// EXTRAS (enum Extras): draft-tree mask words or attention sinks are in use, or
+// a score cap or bias (instantiations of their own, so plain batches run the
+// causal kernel without that code).
+template <class C, int EXTRAS>
 __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                                                    const __grid_constant__ CUtensorMap tmap_v,
                                                                    const __grid_constant__ CUtensorMap tmap_q,
@@ -370,17 +374,20 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
     return a.q_tma != 0 && a.m.qo_indptr[u.b] + (u.row0 + x * kExtendRows) / G + a.q_box_tokens <= total_q;
   };
 
-  if (C::FP8 && (warp == C::kProducerWarp || warp == C::kVProducerWarp)) {
-    // ------------------------------------------------------------ E4M3 producers
+  if (C::CODED && (warp == C::kProducerWarp || warp == C::kVProducerWarp)) {
+    // ------------------------------------------------------------ producers of coded pools
     // Warp 8 streams K, warp 10 V. TMA lands each tile's codes in the raw ring
-    // (one 16-row x 128-byte box per page, 128-byte swizzle); the warp widens
+    // (E4M3: one 16-row x 128-byte box per page, 128-byte swizzle; 4-bit: one
+    // bulk copy per 16-slot tile, as it lies in the pool); the warp widens
     // the rows of the loaded pages to f16 (exact) into the operand ring, in
     // the operand layout (two 64-column blocks, 128-byte swizzle), and marks
     // the operand tile full. A raw slot is requested again as soon as the warp
     // has read it, R tiles ahead of the widening. Warp 8 also hands Q over.
     const bool is_v = warp == C::kVProducerWarp;
     const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
-    if (elect_one()) prefetch_tmap(tmap);
+    const uint8_t* pool = is_v ? a.v_pool : a.k_pool;
+    constexpr int kSegBytes = C::FP4 ? fp4_tile_bytes(DK) : kSegSlots * 128;  // raw bytes of 16 slots
+    if (!C::FP4 && elect_one()) prefetch_tmap(tmap);
     const int R = is_v ? C::RV : C::RK;
     const int depth = is_v ? NV : NK;
     uint64_t* rfull = is_v ? raw_full + C::RK : raw_full;
@@ -436,13 +443,21 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         const int npg = min(kPagesPerTile, np - j * kPagesPerTile);
         const int rs = (int)(rt % R);
         const bool leader = elect_one();
-        if (leader) mbar_arrive_expect_tx(&rfull[rs], (uint32_t)(npg * kSegSlots * 128));
+        if (leader) mbar_arrive_expect_tx(&rfull[rs], (uint32_t)(npg * kSegBytes));
         uint8_t* dst = raw_ring + rs * C::kRawTileBytes;
+        if constexpr (C::FP4) {
+          __syncwarp();
+          const int pg = __shfl_sync(0xffffffffu, grp, ((e & 3) << 3) + (lane & 7));
+          if (lane < npg && !(hold_first && rt == 0))
+            bulk_load_hint(dst + lane * kSegBytes, pool + ((long long)pg * a.num_kv_heads + g) * kSegBytes, kSegBytes,
+                           &rfull[rs], pol);
+        } else {
 #pragma unroll
-        for (int p = 0; p < kPagesPerTile; ++p) {
-          const int pg = __shfl_sync(0xffffffffu, grp, ((e & 3) << 3) + p);
-          if (p < npg && leader && !(hold_first && rt == 0))
-            tma_load_2d_hint(dst + p * (kSegSlots * 128), tmap, g * 128, pg * kSegSlots, &rfull[rs], pol);
+          for (int p = 0; p < kPagesPerTile; ++p) {
+            const int pg = __shfl_sync(0xffffffffu, grp, ((e & 3) << 3) + p);
+            if (p < npg && leader && !(hold_first && rt == 0))
+              tma_load_2d_hint(dst + p * kSegBytes, tmap, g * 128, pg * kSegSlots, &rfull[rs], pol);
+          }
         }
         ++rt;
         ++issued;
@@ -482,14 +497,38 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         const uint32_t src = raw_base + rs * C::kRawTileBytes;
         const uint32_t out_blk = op_base + st * kOpTile + (c >> 2) * (kExtendKeys * 128);
         // lane: chunk c (codes 16c .. 16c + 15) of rows r0 + 4k; one 16-byte
-        // chunk in, f16 chunks 2c and 2c + 1 of column block c / 4 out. Four
-        // rows a group, the next group's chunks loaded before this one is widened.
+        // chunk in (4-bit: 8 bytes and the block's scale), f16 chunks 2c and
+        // 2c + 1 of column block c / 4 out. Four rows a group, the next
+        // group's chunks loaded before this one is widened.
         auto ld = [&](int k) {
           const int r = r0 + 4 * k;
-          return lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
+          if constexpr (C::FP4) {
+            const uint32_t seg = src + (r / kSegSlots) * kSegBytes;
+            const int i = r % kSegSlots;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            uint16_t s;
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(seg + i * 64 + c * 8));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=h"(s) : "r"(seg + kSegSlots * 64 + i * 8 + c));
+            x.z = s;
+            return x;
+          } else {
+            return lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
+          }
         };
         auto widen = [&](int k, const uint4& x) {
           const int r = r0 + 4 * k;
+          if constexpr (C::FP4) {
+            const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(x.z | (x.z << 8)));
+            uint32_t w[8];
+            e2m1x8_to_f16x2(x.x, w);
+            e2m1x8_to_f16x2(x.y, w + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = mul_f16x2(w[i], s2);  // exact: at most 6 significant bits
+            const uint32_t row = out_blk + r * 128;
+            sts128(row + ((((2 * c) & 7) ^ (r & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+            sts128(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4), make_uint4(w[4], w[5], w[6], w[7]));
+            return;
+          }
           const uint4 lo = make_uint4(e4m3x2_to_f16x2((uint16_t)(x.x & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(x.x >> 16)),
                                       e4m3x2_to_f16x2((uint16_t)(x.y & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(x.y >> 16)));
           const uint4 hi = make_uint4(e4m3x2_to_f16x2((uint16_t)(x.z & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(x.z >> 16)),
@@ -663,9 +702,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
     // The whole warp runs the loop and one elected lane issues each tcgen05
     // instruction. Descriptors: the start-address field is the low bits, so a
     // byte offset b inside the tile adds b >> 4.
-    constexpr uint32_t idesc_qk = C::FP8 ? umma_idesc_f16(kExtendRows, kExtendKeys, false, false)
+    constexpr uint32_t idesc_qk = C::CODED ? umma_idesc_f16(kExtendRows, kExtendKeys, false, false)
                                          : umma_idesc_bf16(kExtendRows, kExtendKeys, false, false);
-    constexpr uint32_t idesc_pv = C::FP8 ? umma_idesc_f16(kExtendRows, DV, false, true)
+    constexpr uint32_t idesc_pv = C::CODED ? umma_idesc_f16(kExtendRows, DV, false, true)
                                          : umma_idesc_bf16(kExtendRows, DV, false, true);
     const uint64_t q_desc0 = umma_desc_sw128(smem_base + C::kQOff, 16, 1024);
     const uint64_t k_desc0 = umma_desc_sw128(smem_base + C::kKOff, 16, 1024);
@@ -832,7 +871,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
       // draft trees: the row's mask word clears the drafts outside its tree
       uint64_t tword = ~0ull;
       int draft0 = 0x3fffffff;  // first draft key (none without a tree)
-      if constexpr (EXTRAS) {
+      float slope = 0.f;  // distance slope of the row's head, in the log2 domain
+      if constexpr (EXTRAS == kExtrasScores) {
+        if (a.mods.slopes) slope = a.mods.slopes[g * G + R % G] * kLog2e;
+      }
+      if constexpr (EXTRAS != kExtrasNone) {
         if (a.tree) {
           tword = valid ? a.tree[q0 + R / G] : ~0ull;
           draft0 = L - qo;
@@ -868,7 +911,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
             for (int c = 0; c < DV; c += 8)
               *reinterpret_cast<uint4*>(a.out + orow * DV + c) = make_uint4(0, 0, 0, 0);
             // no key: the LSE is the sink's alone
-            if (a.lse) a.lse[orow] = (EXTRAS && a.sinks) ? a.sinks[g * G + R % G] : -INFINITY;
+            if (a.lse) a.lse[orow] = (EXTRAS != kExtrasNone && a.sinks) ? a.sinks[g * G + R % G] : -INFINITY;
           }
         }
         jt += ukv.len();
@@ -887,7 +930,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<uint4*>(qtile + h * (kExtendRows * 128) + r * 128 + ((c ^ (r & 7)) << 4)) =
-                C::FP8 ? bf16x8_to_f16x8(v[c]) : v[c];
+                C::CODED ? bf16x8_to_f16x8(v[c]) : v[c];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -909,7 +952,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         const int key0 = j * kExtendKeys;
         // some keys of this tile are masked for this row: past its limit, or
         // drafts that its tree may hide
-        const bool diag = key0 + kExtendKeys - 1 > limit || (EXTRAS && key0 + kExtendKeys > draft0);
+        const bool diag =
+            key0 + kExtendKeys - 1 > limit || (EXTRAS != kExtrasNone && key0 + kExtendKeys > draft0);
         // the request's last page inside this KV tile: zero the V rows past L
         // (done by the first tile that reads this V tile, before its PV)
         if ((ukv.dual || x == 0 || jr >= nA) && np <= (j + 1) * kPagesPerTile && (L % kSegSlots) != 0) {
@@ -930,15 +974,33 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
           }
           fence_proxy_async_smem();
         }
-        const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
+        // (scores with a cap or bias leave load_s in the log2 domain)
+        const float scale = EXTRAS == kExtrasScores ? 1.f : a.scale_log2;
+        const uint64_t sc2 = f2_pack(scale, scale);
         uint32_t pk[kExtendKeys / 2];  // P as bf16 pairs, written to TMEM once final
         // S read 64 columns per TMEM wait; masked keys become -inf
         auto load_s = [&](int cc, uint32_t* sr) {
           tmem_ld32(lane_base + s_col + cc * 32, sr);
           tmem_ld32(lane_base + s_col + cc * 32 + 32, sr + 32);
           tmem_wait_ld();
+          if constexpr (EXTRAS == kExtrasScores) {
+            // score cap, then distance bias (one uniform branch for the 64 scores)
+            if (a.mods.cap2 != 0.f) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) sr[i] = __float_as_uint(capped_score(a.mods, __uint_as_float(sr[i])));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) * a.scale_log2);
+            }
+            if (a.mods.slopes) {
+              const float d0 = (float)(key0 + cc * 32 - limit);
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                sr[i] = __float_as_uint(fmaf(slope, d0 + (float)i, __uint_as_float(sr[i])));
+            }
+          }
           if (diag) {
-            if constexpr (EXTRAS) {
+            if constexpr (EXTRAS != kExtrasNone) {
               mask32_bits(sr, visible32(key0 + cc * 32, limit, draft0, tword));
               mask32_bits(sr + 32, visible32(key0 + cc * 32 + 32, limit, draft0, tword));
             } else {
@@ -955,8 +1017,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
           for (int cc = 0; cc < kExtendKeys / 32; cc += 2) {
             uint32_t sr[64];
             load_s(cc, sr);
-            exp32<C::FP8>(sr, sc2, nref2, pk + cc * 16, acc);
-            exp32<C::FP8>(sr + 32, sc2, nref2, pk + cc * 16 + 16, acc);
+            exp32<C::CODED>(sr, sc2, nref2, pk + cc * 16, acc);
+            exp32<C::CODED>(sr + 32, sc2, nref2, pk + cc * 16 + 16, acc);
           }
           const uint64_t accs = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
           return f2_lo(accs) + f2_hi(accs);
@@ -972,7 +1034,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         // so the whole warp takes this branch when any of its rows needs it;
         // the other rows keep their reference and get the same P again. A row
         // that sees no key of this tile (limit < key0) never needs it.
-        constexpr float kHigh = C::FP8 ? kSumHighF16 : kSumHigh, kLow = C::FP8 ? kSumLowF16 : kSumLow;
+        constexpr float kHigh = C::CODED ? kSumHighF16 : kSumHigh, kLow = C::CODED ? kSumLowF16 : kSumLow;
         const bool need = (!(tsum <= kHigh) || (l == 0.f && tsum < kLow)) && limit >= key0;
         if (__any_sync(0xffffffffu, need)) {
           float mx = -INFINITY;
@@ -982,7 +1044,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
             load_s(cc, sr);
             mx = max32(sr + 32, max32(sr, mx));
           }
-          const float mt = mx * a.scale_log2;
+          const float mt = mx * scale;
           const bool move = need && mt != -INFINITY && (mt > m_ref || l == 0.f);
           // O_X holds every earlier PV: the s_full commit waited on above was
           // issued after PV_X of the previous tile
@@ -1059,8 +1121,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         m_ref = m;
       }
       float inv = l > 0.f ? 1.f / l : 0.f;
-      if constexpr (C::FP8) inv *= a.v_scale;  // V codes times the pool's scale
-      if constexpr (EXTRAS) {
+      if constexpr (C::CODED) inv *= a.v_scale;  // V codes times the pool's scale
+      if constexpr (EXTRAS != kExtrasNone) {
         // final rows of a model with sinks: the head's sink joins the normaliser
         if (!split && valid && a.sinks) {
           float lse_s = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
@@ -1121,7 +1183,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
       }
       if (valid) {
         float lse_v = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
-        if constexpr (EXTRAS) {
+        if constexpr (EXTRAS != kExtrasNone) {
           if (!split && a.sinks) (void)sink_factor(lse_v, a.sinks[g * G + R % G]);
         }
         if (split)
@@ -1145,19 +1207,22 @@ template <class C>
 int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, float sm_scale, float k_scale,
                float v_scale, void* out, float* lse, cudaStream_t st, bool dplan) {
   CUtensorMap tk, tv;
+  memset(&tk, 0, sizeof(tk));
+  memset(&tv, 0, sizeof(tv));
   const uint64_t inner_k = (uint64_t)c.cfg.num_kv_heads * C::DK;
   const uint64_t inner_v = (uint64_t)c.cfg.num_kv_heads * C::DV;
   const uint64_t slots = (uint64_t)c.cfg.num_pages * c.cfg.page_size;
   // boxes of 16 slots x 128 bytes: 64 bf16 elements, or 128 E4M3 codes (the
   // whole row of a 128-wide head)
-  const CUtensorMapDataType dt = C::FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const uint32_t esz = C::FP8 ? 1 : 2;
+  const CUtensorMapDataType dt = C::CODED ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint32_t esz = C::CODED ? 1 : 2;
   // L2 fills no wider than one head's row of an E4M3 pool (128 bytes)
-  const CUtensorMapL2promotion promo = C::FP8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-  if (encode_tmap_2d(&tk, dt, const_cast<void*>(k_pool), inner_k, slots, inner_k * esz, 128 / esz, kSegSlots,
-                     CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
+  const CUtensorMapL2promotion promo = C::CODED ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  // (4-bit tiles come by untiled bulk copies)
+  if (!C::FP4 && encode_tmap_2d(&tk, dt, const_cast<void*>(k_pool), inner_k, slots, inner_k * esz, 128 / esz, kSegSlots,
+                                CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
     return PKV_ERR_CUDA;
-  if (encode_tmap_2d(&tv, dt, const_cast<void*>(v_pool), inner_v, slots, inner_v * esz, 128 / esz, kSegSlots,
+  if (!C::FP4 && encode_tmap_2d(&tv, dt, const_cast<void*>(v_pool), inner_v, slots, inner_v * esz, 128 / esz, kSegSlots,
                      CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
     return PKV_ERR_CUDA;
   ExtendArgs a;
@@ -1168,10 +1233,13 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   a.num_q_heads = c.cfg.num_q_heads;
   a.num_kv_heads = c.cfg.num_kv_heads;
   a.group = c.cfg.num_q_heads / c.cfg.num_kv_heads;
-  // E4M3 codes are widened exactly: the K pool's scale joins the score scale
-  // and the V pool's scale multiplies the output
-  a.scale_log2 = sm_scale * (C::FP8 ? k_scale : 1.f) * kLog2e;
-  a.v_scale = C::FP8 ? v_scale : 1.f;
+  // codes are widened exactly: the K pool's scale joins the score scale and
+  // the V pool's scale multiplies the output
+  a.scale_log2 = sm_scale * (C::CODED ? k_scale : 1.f) * kLog2e;
+  a.v_scale = C::CODED ? v_scale : 1.f;
+  a.mods = score_mods(c, a.scale_log2);
+  a.k_pool = static_cast<const uint8_t*>(k_pool);
+  a.v_pool = static_cast<const uint8_t*>(v_pool);
   a.out_32B = (reinterpret_cast<uintptr_t>(out) & 31) == 0 ? 1 : 0;
   a.tree = active_tree(c);
   a.sinks = c.sinks;
@@ -1184,8 +1252,8 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   memset(&tq, 0, sizeof(tq));
   a.q_tma = 0;
   a.q_box_tokens = 0;
-  // (E4M3 pools: the softmax warps copy Q, converting it to f16 on the way)
-  if (!C::FP8 && kExtendRows % a.group == 0) {
+  // (coded pools: the softmax warps copy Q, converting it to f16 on the way)
+  if (!C::CODED && kExtendRows % a.group == 0) {
     const uint32_t box_tok = kExtendRows / a.group;
     const uint64_t tokens = (uint64_t)(c.cfg.max_q_tokens > (int)box_tok ? c.cfg.max_q_tokens : (int)box_tok);
     if (encode_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void*>(q), C::DK,
@@ -1196,7 +1264,9 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
     a.q_tma = 1;
     a.q_box_tokens = (int)box_tok;
   }
-  auto kernel = (a.tree || a.sinks) ? extend_tc_kernel<C, true> : extend_tc_kernel<C, false>;
+  auto kernel = a.mods.cap2 > 0.f || a.mods.slopes ? extend_tc_kernel<C, kExtrasScores>
+                : a.tree || a.sinks                ? extend_tc_kernel<C, kExtrasMask>
+                                                   : extend_tc_kernel<C, kExtrasNone>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
     return PKV_ERR_CUDA;
   if (launch_pdl(kernel, dim3(c.extend_ctas), dim3(C::kThreads), C::kSmemBytes, st, tk, tv, tq, a) != cudaSuccess)
@@ -1210,12 +1280,18 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
 
 int run_tc(Ctx& c, const void* q, const void* k_pool, const void* v_pool, float sm_scale, float k_scale,
            float v_scale, void* out, float* lse, cudaStream_t st, bool dplan) {
+  if (c.cfg.kv_dtype == PKV_KV_FP4_E2M1) {
+    // 4-bit pools: raw tiles of 9 KB, two K tiles and one V tile in flight
+    if (c.cfg.head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    return run_extend<ExtCfg<128, 128, 2, 2, PKV_KV_FP4_E2M1, 2, 1>>(c, q, k_pool, v_pool, sm_scale, k_scale, v_scale,
+                                                                     out, lse, st, dplan);
+  }
   if (c.cfg.kv_dtype == PKV_KV_FP8_E4M3) {
     // E4M3 pools (128-wide heads): f16 operand rings of two K and two V tiles,
     // one raw tile of codes in flight for each
     if (c.cfg.head_dim != 128) return PKV_ERR_UNSUPPORTED;
-    return run_extend<ExtCfg<128, 128, 2, 2, true, 1, 1>>(c, q, k_pool, v_pool, sm_scale, k_scale, v_scale, out,
-                                                          lse, st, dplan);
+    return run_extend<ExtCfg<128, 128, 2, 2, PKV_KV_FP8_E4M3, 1, 1>>(c, q, k_pool, v_pool, sm_scale, k_scale, v_scale,
+                                                                     out, lse, st, dplan);
   }
   if (c.cfg.head_dim == 128)
     return run_extend<ExtCfg<128, 128, 3, 2>>(c, q, k_pool, v_pool, sm_scale, k_scale, v_scale, out, lse, st, dplan);

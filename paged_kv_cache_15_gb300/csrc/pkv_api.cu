@@ -18,13 +18,15 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+bool known_kv_dtype(int kv) { return kv == PKV_KV_BF16 || kv == PKV_KV_FP8_E4M3 || kv == PKV_KV_FP4_E2M1; }
+
 int check_config(const pkv_config* cfg) {
   if (!cfg) return PKV_ERR_INVALID_ARG;
   if (cfg->num_q_heads <= 0 || cfg->num_kv_heads <= 0 || cfg->head_dim <= 0 || cfg->page_size <= 0 ||
       cfg->num_pages <= 0 || cfg->max_batch <= 0 || cfg->max_pages_total <= 0 || cfg->max_q_tokens <= 0 ||
       cfg->max_qo_len <= 0)
     return PKV_ERR_INVALID_ARG;
-  if (cfg->kv_dtype != PKV_KV_BF16 && cfg->kv_dtype != PKV_KV_FP8_E4M3) return PKV_ERR_INVALID_ARG;
+  if (!known_kv_dtype(cfg->kv_dtype)) return PKV_ERR_INVALID_ARG;
   if (cfg->num_q_heads % cfg->num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
   const int group = cfg->num_q_heads / cfg->num_kv_heads;
   if (group > 16) return PKV_ERR_UNSUPPORTED;
@@ -33,8 +35,9 @@ int check_config(const pkv_config* cfg) {
   // head widths: 64/64, 128/128, and 192/128 (K and V heads of different widths)
   const int dk = cfg->head_dim, dv = head_dim_v(*cfg);
   if (!((dk == 64 && dv == 64) || (dk == 128 && dv == 128) || (dk == 192 && dv == 128))) return PKV_ERR_UNSUPPORTED;
-  // E4M3 pools: 128-wide heads (an E4M3 row of 128 codes is one 128-byte span)
-  if (cfg->kv_dtype == PKV_KV_FP8_E4M3 && dk != 128) return PKV_ERR_UNSUPPORTED;
+  // E4M3 pools: 128-wide heads (an E4M3 row of 128 codes is one 128-byte span),
+  // 4-bit pools likewise (a tile of 16 rows is nine 128-byte lines)
+  if (cfg->kv_dtype != PKV_KV_BF16 && dk != 128) return PKV_ERR_UNSUPPORTED;
   if (decode_row_warps(*cfg) == 0) return PKV_ERR_UNSUPPORTED;  // max_qo_len * group > 128
   // slot indices and pool element offsets must fit the kernels' index types
   const long long slots = (long long)cfg->num_pages * cfg->page_size;
@@ -140,10 +143,10 @@ int get_encoder() {
 }
 
 // Masked scores become -inf before the scale multiplies them: the scales
-// must be positive (k_scale and v_scale matter only for E4M3 pools).
+// must be positive (k_scale and v_scale matter only for E4M3 and 4-bit pools).
 int check_scales(const Ctx& c, float sm_scale, float k_scale, float v_scale) {
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return PKV_ERR_INVALID_ARG;
-  if (c.cfg.kv_dtype == PKV_KV_FP8_E4M3 &&
+  if (c.cfg.kv_dtype != PKV_KV_BF16 &&
       (!(k_scale > 0.f) || !std::isfinite(k_scale) || !(v_scale > 0.f) || !std::isfinite(v_scale)))
     return PKV_ERR_INVALID_ARG;
   return PKV_OK;
@@ -260,7 +263,13 @@ int pkv_pool_bytes(const pkv_config* cfg, size_t* bytes_out) {
   if (!cfg || !bytes_out || cfg->num_pages < 0 || cfg->page_size <= 0 || cfg->num_kv_heads <= 0 ||
       cfg->head_dim <= 0)
     return PKV_ERR_INVALID_ARG;
-  if (cfg->kv_dtype != PKV_KV_BF16 && cfg->kv_dtype != PKV_KV_FP8_E4M3) return PKV_ERR_INVALID_ARG;
+  if (!known_kv_dtype(cfg->kv_dtype)) return PKV_ERR_INVALID_ARG;
+  if (cfg->kv_dtype == PKV_KV_FP4_E2M1) {
+    const size_t slots = (size_t)cfg->num_pages * cfg->page_size;
+    if (slots % kSegSlots != 0 || cfg->head_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    *bytes_out = slots / kSegSlots * cfg->num_kv_heads * fp4_tile_bytes(cfg->head_dim);
+    return PKV_OK;
+  }
   const size_t elem = cfg->kv_dtype == PKV_KV_FP8_E4M3 ? 1 : 2;
   *bytes_out = (size_t)cfg->num_pages * cfg->page_size * cfg->num_kv_heads * cfg->head_dim * elem;
   return PKV_OK;
@@ -353,7 +362,63 @@ int pkv_set_kv_buffer(pkv_ctx* ctx, void* d_k_pool, void* d_v_pool, const int32_
   if (n_tokens == 0) return PKV_OK;
   if (!d_k_pool || !d_v_pool || !d_loc || !d_k || !d_v) return PKV_ERR_INVALID_ARG;
   if (!aligned16(d_k_pool) || !aligned16(d_v_pool) || !aligned16(d_k) || !aligned16(d_v)) return PKV_ERR_INVALID_ARG;
+  if (ctx->cfg.kv_dtype == PKV_KV_FP4_E2M1)
+    return launch_rope_set_kv(*ctx, nullptr, d_k_pool, d_v_pool, d_loc, nullptr, nullptr, 0, d_k,
+                              (long long)ctx->cfg.num_kv_heads * ctx->cfg.head_dim, d_v,
+                              (long long)ctx->cfg.num_kv_heads * head_dim_v(ctx->cfg), nullptr, n_tokens, k_inv_scale,
+                              v_inv_scale, static_cast<cudaStream_t>(stream));
   return launch_set_kv_buffer(*ctx, d_k_pool, d_v_pool, d_loc, d_k, d_v, n_tokens, k_inv_scale, v_inv_scale,
+                              static_cast<cudaStream_t>(stream));
+}
+
+int pkv_rope_set_kv_buffer(pkv_ctx* ctx, const pkv_rope* rope, void* d_k_pool, void* d_v_pool, const int32_t* d_loc,
+                           const int32_t* d_positions, const void* d_q, int64_t q_stride, const void* d_k,
+                           int64_t k_stride, const void* d_v, int64_t v_stride, void* d_q_out, int32_t n_tokens,
+                           float k_inv_scale, float v_inv_scale, void* stream) {
+  if (!ctx || !rope || n_tokens < 0) return PKV_ERR_INVALID_ARG;
+  const pkv_config& c = ctx->cfg;
+  if (rope->rotary_dim <= 0 || rope->rotary_dim % 16 != 0 || rope->rotary_offset < 0 || rope->rotary_offset % 8 != 0 ||
+      rope->rotary_offset > c.head_dim - rope->rotary_dim || rope->max_positions <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (c.kv_dtype != PKV_KV_BF16 && (!(k_inv_scale > 0.f) || !std::isfinite(k_inv_scale) || !(v_inv_scale > 0.f) ||
+                                    !std::isfinite(v_inv_scale)))
+    return PKV_ERR_INVALID_ARG;
+  if (n_tokens == 0) return PKV_OK;
+  if (!rope->d_cos_sin || !d_k_pool || !d_v_pool || !d_loc || !d_positions || !d_k || !d_v) return PKV_ERR_INVALID_ARG;
+  if ((d_q == nullptr) != (d_q_out == nullptr)) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(rope->d_cos_sin) || !aligned16(d_k_pool) || !aligned16(d_v_pool) || !aligned16(d_k) ||
+      !aligned16(d_v) || !aligned16(d_q) || !aligned16(d_q_out))
+    return PKV_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(d_loc) & 3) || (reinterpret_cast<uintptr_t>(d_positions) & 3))
+    return PKV_ERR_INVALID_ARG;
+  const int64_t qw = (int64_t)c.num_q_heads * c.head_dim, kw = (int64_t)c.num_kv_heads * c.head_dim,
+                vw = (int64_t)c.num_kv_heads * head_dim_v(c);
+  auto stride_ok = [](int64_t s, int64_t width) { return s >= width && s % 8 == 0 && s <= (1ll << 40); };
+  if (!stride_ok(k_stride, kw) || !stride_ok(v_stride, vw) || (d_q && !stride_ok(q_stride, qw)))
+    return PKV_ERR_INVALID_ARG;
+  // q_out holds whole rows that other threads still read their inputs from
+  auto overlaps = [&](const void* in, int64_t stride, int64_t width) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(in), a1 = a0 + 2 * ((uintptr_t)stride * (n_tokens - 1) + width);
+    const uintptr_t b0 = reinterpret_cast<uintptr_t>(d_q_out), b1 = b0 + 2 * (uintptr_t)qw * n_tokens;
+    return a0 < b1 && b0 < a1;
+  };
+  if (d_q && (overlaps(d_q, q_stride, qw) || overlaps(d_k, k_stride, kw) || overlaps(d_v, v_stride, vw)))
+    return PKV_ERR_INVALID_ARG;
+  return launch_rope_set_kv(*ctx, rope, d_k_pool, d_v_pool, d_loc, d_positions, d_q, q_stride, d_k, k_stride, d_v,
+                            v_stride, d_q_out, n_tokens, k_inv_scale, v_inv_scale, static_cast<cudaStream_t>(stream));
+}
+
+int pkv_get_kv_buffer(pkv_ctx* ctx, const void* d_k_pool, const void* d_v_pool, const int32_t* d_loc, void* d_k,
+                      void* d_v, int32_t n_tokens, float k_scale, float v_scale, void* stream) {
+  if (!ctx || n_tokens < 0) return PKV_ERR_INVALID_ARG;
+  int st = check_scales(*ctx, 1.f, k_scale, v_scale);
+  if (st != PKV_OK) return st;
+  if (n_tokens == 0) return PKV_OK;
+  if (!d_k_pool || !d_v_pool || !d_loc || !d_k || !d_v) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(d_k_pool) || !aligned16(d_v_pool) || !aligned16(d_k) || !aligned16(d_v) ||
+      (reinterpret_cast<uintptr_t>(d_loc) & 3))
+    return PKV_ERR_INVALID_ARG;
+  return launch_get_kv_buffer(*ctx, d_k_pool, d_v_pool, d_loc, d_k, d_v, n_tokens, k_scale, v_scale,
                               static_cast<cudaStream_t>(stream));
 }
 
@@ -364,6 +429,8 @@ int pkv_forward_decode(pkv_ctx* ctx, const void* d_q, const void* d_k_pool, cons
   st = check_scales(*ctx, sm_scale, k_scale, v_scale);
   if (st != PKV_OK) return st;
   if (ctx->batch == 0) return PKV_OK;
+  // a tree's drafts have no single distance to their ancestors' slots
+  if (ctx->slopes && active_tree(*ctx)) return PKV_ERR_UNSUPPORTED;
   return launch_decode(*ctx, d_q, d_k_pool, d_v_pool, sm_scale, k_scale, v_scale, d_out, d_lse,
                        static_cast<cudaStream_t>(stream));
 }
@@ -375,6 +442,8 @@ int pkv_forward_extend(pkv_ctx* ctx, const void* d_q, const void* d_k_pool, cons
   st = check_scales(*ctx, sm_scale, k_scale, v_scale);
   if (st != PKV_OK) return st;
   if (ctx->batch == 0) return PKV_OK;
+  // a tree's drafts have no single distance to their ancestors' slots
+  if (ctx->slopes && active_tree(*ctx)) return PKV_ERR_UNSUPPORTED;
   return launch_extend(*ctx, d_q, d_k_pool, d_v_pool, sm_scale, k_scale, v_scale, d_out, d_lse,
                        static_cast<cudaStream_t>(stream));
 }
@@ -403,6 +472,19 @@ int pkv_set_attention_sinks(pkv_ctx* ctx, const float* d_sinks) {
   if (!ctx) return PKV_ERR_INVALID_ARG;
   if (d_sinks && (reinterpret_cast<uintptr_t>(d_sinks) & 3u) != 0) return PKV_ERR_INVALID_ARG;
   ctx->sinks = d_sinks;
+  return PKV_OK;
+}
+
+int pkv_set_logit_cap(pkv_ctx* ctx, float cap) {
+  if (!ctx || !(cap >= 0.f) || !std::isfinite(cap)) return PKV_ERR_INVALID_ARG;
+  ctx->logit_cap = cap;
+  return PKV_OK;
+}
+
+int pkv_set_alibi_slopes(pkv_ctx* ctx, const float* d_slopes) {
+  if (!ctx) return PKV_ERR_INVALID_ARG;
+  if (d_slopes && (reinterpret_cast<uintptr_t>(d_slopes) & 3u) != 0) return PKV_ERR_INVALID_ARG;
+  ctx->slopes = d_slopes;
   return PKV_OK;
 }
 
@@ -457,7 +539,10 @@ int pkv_describe(pkv_ctx* ctx, char* buf, size_t n) {
            "pkv sm_103a: heads %d/%d (group %d) head_dim %d/%d page_size %d kv %s pool_pages %d | decode: %s | "
            "extend: tcgen05 %dx%d tiles, grid %d | SMs %d",
            c.num_q_heads, c.num_kv_heads, group, c.head_dim, head_dim_v(c), c.page_size,
-           c.kv_dtype == PKV_KV_FP8_E4M3 ? "fp8_e4m3" : "bf16", c.num_pages, dec, kExtendRows, kExtendKeys,
+           c.kv_dtype == PKV_KV_FP8_E4M3   ? "fp8_e4m3"
+           : c.kv_dtype == PKV_KV_FP4_E2M1 ? "fp4_e2m1"
+                                           : "bf16",
+           c.num_pages, dec, kExtendRows, kExtendKeys,
            ctx->extend_ctas, ctx->num_sms);
   return PKV_OK;
 }

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -107,6 +108,8 @@ struct Ctx {
   int device;
   const uint64_t* tree = nullptr;  // draft-tree mask words (pkv_set_tree_mask), or null
   const float* sinks = nullptr;    // per-query-head sink logits (pkv_set_attention_sinks), or null
+  float logit_cap = 0.f;           // tanh cap of the scores (pkv_set_logit_cap), 0: none
+  const float* slopes = nullptr;   // per-query-head distance slopes (pkv_set_alibi_slopes), or null
 };
 
 // Width of the V heads and of the output rows (head_dim_v, 0 meaning head_dim).
@@ -115,6 +118,33 @@ inline int head_dim_v(const pkv_config& c) { return c.head_dim_v > 0 ? c.head_di
 // The tree mask the next forward applies: only after a build in a verify mode.
 inline const uint64_t* active_tree(const Ctx& c) {
   return (c.mode == PKV_MODE_TARGET_VERIFY || c.mode == PKV_MODE_DRAFT_EXTEND) ? c.tree : nullptr;
+}
+
+// Which instantiation of the attention kernels a forward takes: plain batches
+// run without the code of the features they do not use.
+enum Extras : int { kExtrasNone = 0, kExtrasMask = 1, kExtrasScores = 2 };  // 1: tree or sinks, 2: score changes too
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Score changes of pkv_set_logit_cap and pkv_set_alibi_slopes, in the log2
+// domain: with t = raw * scale_log2,
+//   cap:   t <- cap2 * tanh(t / cap2) = cap2 - 2 * cap2 / (1 + 2^(raw * cap_k))
+//   bias:  t <- t + slope * log2(e) * (key position - query position)
+// The quotient form loses nothing that matters: its absolute error is about
+// 2^-22 * cap2 (cap2 is cap * log2 e), 2e-5 for a cap of 50.
+struct ScoreMods {
+  float cap2;           // cap * log2(e); 0: no cap
+  float cap_k;          // 2 * scale_log2 / cap2 * log2(e)
+  const float* slopes;  // per query head, or null
+};
+
+inline ScoreMods score_mods(const Ctx& c, float scale_log2) {
+  ScoreMods m;
+  m.cap2 = c.logit_cap * kLog2e;
+  m.cap_k = c.logit_cap > 0.f ? 2.f * scale_log2 / c.logit_cap : 0.f;
+  m.slopes = c.slopes;
+  return m;
 }
 
 // Device-side view of the metadata in the workspace.
@@ -139,11 +169,21 @@ struct Meta {
 
 Meta make_meta(const Ctx& c);
 
+// Bytes of one tile of a 4-bit pool: 16 rows of codes, then 16 rows of scales.
+__host__ __device__ constexpr int fp4_tile_bytes(int width) { return kSegSlots * (width / 2 + width / 16); }
+
 // Entry points of the kernels' host launchers (one per translation unit).
 int launch_build_metadata(Ctx& c, int batch, const int32_t* seq_lens, const int32_t* qo_lens,
                           const int32_t* page_table, int stride, cudaStream_t st);
 int launch_set_kv_buffer(Ctx& c, void* k_pool, void* v_pool, const int32_t* loc, const void* k, const void* v,
                          int n, float k_inv, float v_inv, cudaStream_t st);
+// rope null: no rotation (the append into 4-bit pools); q null: k and v alone
+int launch_rope_set_kv(Ctx& c, const pkv_rope* rope, void* k_pool, void* v_pool, const int32_t* loc,
+                       const int32_t* pos, const void* q, long long q_stride, const void* k, long long k_stride,
+                       const void* v, long long v_stride, void* q_out, int n, float k_inv, float v_inv,
+                       cudaStream_t st);
+int launch_get_kv_buffer(Ctx& c, const void* k_pool, const void* v_pool, const int32_t* loc, void* k, void* v, int n,
+                         float k_scale, float v_scale, cudaStream_t st);
 int launch_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, float sm_scale, float k_scale,
                   float v_scale, void* out, float* lse, cudaStream_t st);
 int launch_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, float sm_scale, float k_scale,
@@ -309,6 +349,16 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// Untiled bulk copy of a contiguous run (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                               uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
@@ -381,6 +431,21 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
   return r;
 }
 
+// Eight E2M1 codes (low nibble first) -> four f16x2 registers (exact).
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t v, uint32_t* r) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(v));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Attention sink: the head's sink logit joins the softmax as a key with a zero
 // value vector. Given a finished row's natural-log LSE over its keys, returns
 // the factor that scales its output and moves lse to include the sink (a row
@@ -397,6 +462,17 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A raw score, capped, in the log2 domain.
+__device__ __forceinline__ float capped_score(const ScoreMods& m, float raw) {
+  return m.cap2 - 2.f * m.cap2 * fast_rcp(1.f + fast_exp2(raw * m.cap_k));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

@@ -1,0 +1,412 @@
+// Rotation of q and k by position with the append of k and v to the paged
+// pools in the same pass; the append into 4-bit pools; and the read-back of
+// pool rows.
+//
+//   (a, b) -> (a cos - b sin, b cos + a sin)         columns paired as pkv_rope says
+//   pool[loc] = bf16(y) | e4m3(y * inv) | 4-bit block of y * inv
+//
+// 4-bit block of 16 columns: S = e4m3(max|y| / 6), code = e2m1(y / S), the
+// division as a multiply by the fp32 reciprocal of S. Products and sums of the
+// rotation are rounded one by one (no fused multiply-add), so the stored codes
+// are those of the same formula in elementary fp32 operations, bit for bit.
+//
+// Bound by memory: q, k and v are read once, q_out and the pool rows written
+// once. One thread owns 16 columns of a head (a whole 4-bit block, 32 bytes of
+// bf16) and runs over RPT heads of its token with the angles of those columns
+// in registers; the partner columns of the half-split pairing are read a
+// second time, from L1.
+#include <cmath>
+
+#include "pkv_internal.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 128;
+
+enum Rot { kRotNone = 0, kRotHalf = 1, kRotInterleaved = 2 };
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ void widen8(const uint4& v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 narrow8(const float* x) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 16 scaled values -> 8 code bytes and the block's E4M3 scale byte
+__device__ __forceinline__ uint2 quant_fp4(const float* y, uint8_t* scale) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a = max_nan(a, fabsf(y[i]));
+  const uint16_t s8 = e4m3x2(__fmul_rn(a, 1.0f / 6.0f), 0.f);
+  *scale = (uint8_t)(s8 & 0xff);
+  const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(s8) & 0xffffu)));
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = __fmul_rn(y[8 * k + i], r);
+    asm("{\n .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        " mov.b32 %0, {a, b, c, d};\n}"
+        : "=r"(w[k])
+        : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+struct RopeKvArgs {
+  const uint16_t *q, *k, *v;  // bf16 rows, token i at i * stride elements
+  long long q_stride, k_stride, v_stride;
+  uint16_t* q_out;
+  void *k_pool, *v_pool;
+  const int *loc, *pos;
+  const float* cos_sin;
+  int max_pos, rotary, first;
+  int num_q_heads, num_kv_heads;
+  int q_units, kv_units;  // units (RPT heads) of q, and of k or v, in a token
+  long long n_threads;
+  long long num_slots;
+  float k_inv, v_inv;
+  int* plan;
+};
+
+// Row `head` of width D at a slot (or token): 16 columns (block cb) stored as
+// bf16, or scaled and rounded to the pool's codes.
+template <int D>
+__device__ __forceinline__ void store_bf16(void* rows, long long slot, int heads, int head, int cb, const uint4& x0,
+                                           const uint4& x1) {
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(rows) + (slot * heads + head) * D + cb * 16);
+  dst[0] = x0;
+  dst[1] = x1;
+}
+
+template <int D, int KV>
+__device__ __forceinline__ void store_coded(void* pool, long long slot, int heads, int head, int cb, const float* x,
+                                            float inv) {
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(x[i], inv);
+  if constexpr (KV == PKV_KV_FP8_E4M3) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = (uint32_t)e4m3x2(y[4 * i], y[4 * i + 1]) | ((uint32_t)e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(pool) + (slot * heads + head) * D + cb * 16) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    uint8_t s;
+    const uint2 codes = quant_fp4(y, &s);
+    uint8_t* tile = static_cast<uint8_t*>(pool) + ((slot / kSegSlots) * heads + head) * fp4_tile_bytes(D);
+    const int r = (int)(slot % kSegSlots);
+    *reinterpret_cast<uint2*>(tile + r * (D / 2) + cb * 8) = codes;
+    tile[kSegSlots * (D / 2) + r * (D / 16) + cb] = s;
+  }
+}
+
+template <int DK, int DV, int KV, int ROT, int RPT>
+__global__ void __launch_bounds__(kThreads) rope_kv_kernel(RopeKvArgs a) {
+  constexpr int CB = DK / 16;  // threads of a unit: 16 columns each
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long t = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (t >= a.n_threads) return;
+  const int per_token = a.q_units + 2 * a.kv_units;
+  const long long unit = t / CB;
+  const int cb = (int)(t - unit * CB);
+  const long long tok = unit / per_token;
+  int u = (int)(unit - tok * per_token);
+  const int pos = ROT != kRotNone ? a.pos[tok] : 0;
+  const long long slot = a.loc[tok];
+  if (ROT != kRotNone && (pos < 0 || pos >= a.max_pos)) {
+    if (cb == 0 && u == 0) record_error(a.plan, PKV_DEV_BAD_POSITION, (int)tok);
+    return;
+  }
+  const bool is_q = u < a.q_units;
+  const bool is_v = u >= a.q_units + a.kv_units;
+  if (!is_q) {
+    u -= is_v ? a.q_units + a.kv_units : a.q_units;
+    if (slot < 0 || slot >= a.num_slots) {
+      if (cb == 0 && u == 0 && !is_v) record_error(a.plan, PKV_DEV_BAD_SLOT, (int)tok);
+      return;
+    }
+  }
+  const int heads = is_q ? a.num_q_heads : a.num_kv_heads;
+  const int h0 = u * RPT, h1 = min(heads, h0 + RPT);
+  if (is_v) {
+    if (cb * 16 >= DV) return;
+    const uint16_t* src = a.v + tok * a.v_stride + cb * 16;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int h = h0 + i;
+      if (h >= h1) break;
+      const uint4* p = reinterpret_cast<const uint4*>(src + h * DV);
+      const uint4 x0 = __ldcs(p), x1 = __ldcs(p + 1);
+      if constexpr (KV == PKV_KV_BF16) {
+        store_bf16<DV>(a.v_pool, slot, heads, h, cb, x0, x1);
+      } else {
+        float x[16];
+        widen8(x0, x);
+        widen8(x1, x + 8);
+        store_coded<DV, KV>(a.v_pool, slot, heads, h, cb, x, a.v_inv);
+      }
+    }
+    return;
+  }
+  // the two 8-column vectors of this thread: rotated or not, partner column,
+  // sign of the sin term, and their cos and sin
+  const int half = a.rotary / 2;
+  float c[16], s[16];
+  int partner[2];
+  bool rot[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const int col = cb * 16 + 8 * v, rel = col - a.first;
+    rot[v] = ROT != kRotNone && rel >= 0 && rel < a.rotary;
+    partner[v] = col;
+    if (!rot[v]) continue;
+    const float* row = a.cos_sin + (long long)pos * a.rotary;
+    if constexpr (ROT == kRotHalf) {
+      const bool low = rel < half;
+      const int j = low ? rel : rel - half;
+      partner[v] = low ? col + half : col - half;
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float4 cc = *reinterpret_cast<const float4*>(row + j + i);
+        const float4 ss = *reinterpret_cast<const float4*>(row + half + j + i);
+        const float sg = low ? -1.f : 1.f;  // (an exact change of sign)
+        c[8 * v + i] = cc.x, c[8 * v + i + 1] = cc.y, c[8 * v + i + 2] = cc.z, c[8 * v + i + 3] = cc.w;
+        s[8 * v + i] = sg * ss.x, s[8 * v + i + 1] = sg * ss.y, s[8 * v + i + 2] = sg * ss.z;
+        s[8 * v + i + 3] = sg * ss.w;
+      }
+    } else {
+      const int j = rel / 2;
+      const float4 cc = *reinterpret_cast<const float4*>(row + j);
+      const float4 ss = *reinterpret_cast<const float4*>(row + half + j);
+      const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[8 * v + 2 * i] = c[8 * v + 2 * i + 1] = cv[i];
+        s[8 * v + 2 * i] = -sv[i];
+        s[8 * v + 2 * i + 1] = sv[i];
+      }
+    }
+  }
+  const uint16_t* src = is_q ? a.q + tok * a.q_stride : a.k + tok * a.k_stride;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int h = h0 + i;
+    if (h >= h1) break;
+    float x[16], y[16];
+    uint4 out[2];  // as bf16; columns that are not rotated keep their bits
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      out[v] = *reinterpret_cast<const uint4*>(src + h * DK + cb * 16 + 8 * v);
+      widen8(out[v], x + 8 * v);
+      float p[8];
+      if constexpr (ROT == kRotHalf) {
+        widen8(*reinterpret_cast<const uint4*>(src + h * DK + partner[v]), p);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = x[8 * v + (e ^ 1)];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        y[8 * v + e] = rot[v] ? __fadd_rn(__fmul_rn(x[8 * v + e], c[8 * v + e]), __fmul_rn(p[e], s[8 * v + e]))
+                              : x[8 * v + e];
+      if (rot[v]) out[v] = narrow8(y + 8 * v);
+    }
+    if (is_q) {
+      store_bf16<DK>(a.q_out, tok, heads, h, cb, out[0], out[1]);
+    } else if constexpr (KV == PKV_KV_BF16) {
+      store_bf16<DK>(a.k_pool, slot, heads, h, cb, out[0], out[1]);
+    } else {
+      store_coded<DK, KV>(a.k_pool, slot, heads, h, cb, y, a.k_inv);
+    }
+  }
+}
+
+template <int DK, int DV, int KV, int ROT>
+int run_rope(RopeKvArgs& a, int n, cudaStream_t st) {
+  // one head a thread while the launch is small (latency), four once there
+  // are enough threads to fill the GPU
+  const long long rows = (long long)n * (a.num_q_heads + 2 * a.num_kv_heads);
+  const int rpt = rows * (DK / 16) >= (1 << 19) ? 4 : 1;
+  a.q_units = a.q ? (a.num_q_heads + rpt - 1) / rpt : 0;
+  a.kv_units = (a.num_kv_heads + rpt - 1) / rpt;
+  a.n_threads = (long long)n * (a.q_units + 2 * a.kv_units) * (DK / 16);
+  const long long blocks = (a.n_threads + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;
+  auto kernel = rpt == 4 ? rope_kv_kernel<DK, DV, KV, ROT, 4> : rope_kv_kernel<DK, DV, KV, ROT, 1>;
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, a) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <int ROT>
+int dispatch_rope(const pkv_config& cfg, RopeKvArgs& a, int n, cudaStream_t st) {
+  if (cfg.kv_dtype == PKV_KV_FP4_E2M1) return run_rope<128, 128, PKV_KV_FP4_E2M1, ROT>(a, n, st);
+  if constexpr (ROT != kRotNone) {
+    if (cfg.kv_dtype == PKV_KV_FP8_E4M3) return run_rope<128, 128, PKV_KV_FP8_E4M3, ROT>(a, n, st);
+    if (cfg.head_dim == 128) return run_rope<128, 128, PKV_KV_BF16, ROT>(a, n, st);
+    if (cfg.head_dim == 64) return run_rope<64, 64, PKV_KV_BF16, ROT>(a, n, st);
+    if (cfg.head_dim == 192) return run_rope<192, 128, PKV_KV_BF16, ROT>(a, n, st);
+  }
+  return PKV_ERR_UNSUPPORTED;
+}
+
+// ---------------------------------------------------------------- read-back
+// One thread reads 16 columns (block cb) of a K or V row and writes them as bf16.
+struct GetKvArgs {
+  const void *k_pool, *v_pool;
+  uint16_t *k, *v;
+  const int* loc;
+  int heads, dk, dv;
+  long long n_threads, num_slots;
+  float k_scale, v_scale;
+  int* plan;
+};
+
+template <int KV>
+__global__ void __launch_bounds__(256) get_kv_kernel(GetKvArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (t >= a.n_threads) return;
+  const int cbs = a.dk / 16;
+  const long long row = t / cbs;
+  const int cb = (int)(t - row * cbs);
+  const long long tok = row / a.heads;
+  const int h = (int)(row - tok * a.heads);
+  const long long slot = a.loc[tok];
+  if (slot < 0 || slot >= a.num_slots) {
+    if (h == 0 && cb == 0) record_error(a.plan, PKV_DEV_BAD_SLOT, (int)tok);
+    return;
+  }
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const int d = which ? a.dv : a.dk;
+    if (cb * 16 >= d) continue;
+    const uint8_t* pool = static_cast<const uint8_t*>(which ? a.v_pool : a.k_pool);
+    const float scale = which ? a.v_scale : a.k_scale;
+    uint4* dst = reinterpret_cast<uint4*>((which ? a.v : a.k) + (tok * a.heads + h) * d + cb * 16);
+    if constexpr (KV == PKV_KV_BF16) {
+      const uint4* src = reinterpret_cast<const uint4*>(pool + ((slot * a.heads + h) * d + cb * 16) * 2);
+      const uint4 x0 = src[0], x1 = src[1];
+      dst[0] = x0;
+      dst[1] = x1;
+    } else {
+      uint32_t w[8];  // 16 values as f16 pairs, exact
+      if constexpr (KV == PKV_KV_FP8_E4M3) {
+        const uint4 x = *reinterpret_cast<const uint4*>(pool + (slot * a.heads + h) * d + cb * 16);
+        const uint32_t c[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[2 * i] = e4m3x2_to_f16x2((uint16_t)(c[i] & 0xffffu));
+          w[2 * i + 1] = e4m3x2_to_f16x2((uint16_t)(c[i] >> 16));
+        }
+      } else {
+        const uint8_t* tile = pool + ((slot / kSegSlots) * a.heads + h) * fp4_tile_bytes(d);
+        const int r = (int)(slot % kSegSlots);
+        const uint2 x = *reinterpret_cast<const uint2*>(tile + r * (d / 2) + cb * 8);
+        const uint32_t s8 = tile[kSegSlots * (d / 2) + r * (d / 16) + cb];
+        const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(s8 | (s8 << 8)));
+        e2m1x8_to_f16x2(x.x, w);
+        e2m1x8_to_f16x2(x.y, w + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = mul_f16x2(w[i], s2);  // exact: at most 6 significant bits
+      }
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float lo = __half2float(__ushort_as_half((unsigned short)(w[i] & 0xffffu)));
+        const float hi = __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
+        o[i] = pack_bf16(__fmul_rn(lo, scale), __fmul_rn(hi, scale));
+      }
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+}  // namespace
+
+int launch_rope_set_kv(Ctx& c, const pkv_rope* rope, void* k_pool, void* v_pool, const int32_t* loc,
+                       const int32_t* pos, const void* q, long long q_stride, const void* k, long long k_stride,
+                       const void* v, long long v_stride, void* q_out, int n, float k_inv, float v_inv,
+                       cudaStream_t st) {
+  RopeKvArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.loc = loc;
+  a.pos = pos;
+  a.cos_sin = rope ? rope->d_cos_sin : nullptr;
+  a.max_pos = rope ? rope->max_positions : 0;
+  a.rotary = rope ? rope->rotary_dim : 0;
+  a.first = rope ? rope->rotary_offset : 0;
+  a.num_q_heads = q ? c.cfg.num_q_heads : 0;
+  a.num_kv_heads = c.cfg.num_kv_heads;
+  a.num_slots = (long long)c.cfg.num_pages * c.cfg.page_size;
+  a.k_inv = k_inv;
+  a.v_inv = v_inv;
+  a.plan = make_meta(c).plan;
+  if (!rope) return dispatch_rope<kRotNone>(c.cfg, a, n, st);
+  return rope->interleaved ? dispatch_rope<kRotInterleaved>(c.cfg, a, n, st)
+                           : dispatch_rope<kRotHalf>(c.cfg, a, n, st);
+}
+
+int launch_get_kv_buffer(Ctx& c, const void* k_pool, const void* v_pool, const int32_t* loc, void* k, void* v, int n,
+                         float k_scale, float v_scale, cudaStream_t st) {
+  GetKvArgs a;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.k = static_cast<uint16_t*>(k);
+  a.v = static_cast<uint16_t*>(v);
+  a.loc = loc;
+  a.heads = c.cfg.num_kv_heads;
+  a.dk = c.cfg.head_dim;  // the K heads are at least as wide as the V heads (check_config)
+  a.dv = head_dim_v(c.cfg);
+  a.n_threads = (long long)n * a.heads * (a.dk / 16);
+  a.num_slots = (long long)c.cfg.num_pages * c.cfg.page_size;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.plan = make_meta(c).plan;
+  const long long blocks = (a.n_threads + 255) / 256;
+  if (blocks > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;
+  auto kernel = c.cfg.kv_dtype == PKV_KV_BF16       ? get_kv_kernel<PKV_KV_BF16>
+                : c.cfg.kv_dtype == PKV_KV_FP8_E4M3 ? get_kv_kernel<PKV_KV_FP8_E4M3>
+                                                    : get_kv_kernel<PKV_KV_FP4_E2M1>;
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(256), 0, st, a) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace pkv

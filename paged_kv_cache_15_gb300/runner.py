@@ -11,6 +11,7 @@ import torch
 from . import binding as B
 from .workloads import Workload
 
+KV_OF = {"bf16": B.PKV_KV_BF16, "fp8_e4m3": B.PKV_KV_FP8_E4M3, "fp4_e2m1": B.PKV_KV_FP4_E2M1}
 MODE_OF = {"decode": B.PKV_MODE_DECODE, "extend": B.PKV_MODE_EXTEND, "verify": B.PKV_MODE_TARGET_VERIFY}
 
 
@@ -21,7 +22,7 @@ def config_for(W: Workload, max_batch=None, max_pages_total=None, max_q_tokens=N
         max_qo_len = int(W.qo_lens.max()) if W.mode == "verify" else 1
         max_qo_len = max(1, min(max_qo_len, 128 // G))
     return B.make_config(W.num_q_heads, W.num_kv_heads, W.head_dim, W.page_size,
-                         B.PKV_KV_FP8_E4M3 if W.is_fp8 else B.PKV_KV_BF16, W.num_pages,
+                         KV_OF[W.kv_dtype], W.num_pages,
                          max_batch or max(W.bs, 1), max_pages_total or max(pages, 1),
                          max_q_tokens or max(W.total_q, 1), max_qo_len, head_dim_v=W.head_dim_v)
 
@@ -58,13 +59,31 @@ class DeviceBatch:
             self.sinks = torch.from_numpy(W.sinks.astype("float32")).to(dev)
             B.pkv_set_attention_sinks(self.ctx, self.sinks)
 
+        # score cap and distance slopes (fp32 per query head)
+        if W.logit_cap:
+            B.pkv_set_logit_cap(self.ctx, W.logit_cap)
+        self.slopes = None
+        if W.slopes is not None:
+            self.slopes = torch.from_numpy(W.slopes.astype("float32")).to(dev)
+            B.pkv_set_alibi_slopes(self.ctx, self.slopes)
+        # rotation of q and k as they are stored: the forward then reads q_rot
+        self.q_rot = None
+        if W.cos_sin is not None:
+            self.cos_sin = torch.from_numpy(W.cos_sin).to(dev)
+            self.positions = torch.from_numpy(W.positions).to(dev)
+            self.q_rot = torch.empty_like(self.q)
+
     @property
     def ctx(self):
         return self.attn.ctx
 
     def set_kv_buffer(self):
         W = self.W
-        if W.loc.shape[0]:
+        if W.cos_sin is not None:
+            B.pkv_rope_set_kv_buffer(self.ctx, self.k_pool, self.v_pool, self.loc, self.positions, self.cos_sin,
+                                     self.q, self.k_new, self.v_new, self.q_rot, W.rotary_offset, W.interleaved,
+                                     W.k_inv_scale, W.v_inv_scale)
+        elif W.loc.shape[0]:
             B.pkv_set_kv_buffer(self.ctx, self.k_pool, self.v_pool, self.loc, self.k_new, self.v_new,
                                 W.k_inv_scale, W.v_inv_scale)
 
@@ -74,7 +93,8 @@ class DeviceBatch:
 
     def forward(self, spec_mode=B.PKV_SPEC_PREFILL, mode=None, lse=True):
         W = self.W
-        B.pkv_forward(self.ctx, self.mode if mode is None else mode, spec_mode, self.q, self.k_pool, self.v_pool,
+        B.pkv_forward(self.ctx, self.mode if mode is None else mode, spec_mode,
+                      self.q if self.q_rot is None else self.q_rot, self.k_pool, self.v_pool,
                       W.sm_scale, self.out, self.lse if lse else None, W.k_scale, W.v_scale)
 
     def step(self, spec_mode=B.PKV_SPEC_PREFILL):

@@ -52,7 +52,7 @@ class Workload:
     num_kv_heads: int
     head_dim: int
     page_size: int
-    kv_dtype: str  # "bf16" | "fp8_e4m3"
+    kv_dtype: str  # "bf16" | "fp8_e4m3" | "fp4_e2m1"
     num_pages: int
     prefix_lens: np.ndarray  # int32 [bs]  tokens already in the pool
     qo_lens: np.ndarray  # int32 [bs]      new tokens (query rows) per request
@@ -60,7 +60,7 @@ class Workload:
     page_table: np.ndarray  # int32 [bs, max_pages]
     loc: np.ndarray  # int32 [n_new]       slots of the new tokens
     q: torch.Tensor  # bf16 [T, Hq, D]
-    k_pool: torch.Tensor  # bf16 or uint8 (E4M3 bits) [slots, Hkv, D]
+    k_pool: torch.Tensor  # bf16 or uint8 (E4M3 bits) [slots, Hkv, D]; 4-bit pools: uint8 [bytes of their tiles]
     v_pool: torch.Tensor
     k_new: torch.Tensor  # bf16 [n_new, Hkv, D]
     v_new: torch.Tensor
@@ -76,6 +76,16 @@ class Workload:
     sinks: Optional[np.ndarray] = None
     # width of the V heads (and of the output rows); 0 means head_dim
     head_dim_v: int = 0
+    # rotation of q and k by position on the way to the pool: None, or fp32
+    # [max_positions, rotary_dim] cosines then sines (rope_table), with the
+    # new tokens' positions (int32 [n_new]) and the pairing of columns
+    cos_sin: Optional[np.ndarray] = None
+    positions: Optional[np.ndarray] = None
+    rotary_offset: int = 0
+    interleaved: bool = False
+    # score cap (0: none) and per-head distance slopes (None, or fp32 [Hq])
+    logit_cap: float = 0.0
+    slopes: Optional[np.ndarray] = None
 
     @property
     def dv(self) -> int:
@@ -100,6 +110,51 @@ class Workload:
     @property
     def is_fp8(self) -> bool:
         return self.kv_dtype == "fp8_e4m3"
+
+    @property
+    def is_fp4(self) -> bool:
+        return self.kv_dtype == "fp4_e2m1"
+
+
+def fp4_pack_rows(values: torch.Tensor, inv_scale: float):
+    """fp32 rows [n, heads, D] -> (codes [n, heads, D], scale bytes [n, heads, D/16]): E2M1 codes (nearest, ties to the
+    even code) of blocks of 16 columns divided by their E4M3 scale max|y| / 6, y = x * inv_scale."""
+    blocks = (values * torch.tensor(inv_scale, dtype=torch.float32)).unflatten(-1, (-1, 16))
+    scale = (blocks.abs().amax(-1) * torch.tensor(1.0 / 6.0, dtype=torch.float32)).clamp(max=E4M3_MAX)
+    scale = scale.to(torch.float8_e4m3fn)
+    s = scale.float()
+    z = blocks * torch.where(s > 0, 1.0 / s, torch.zeros_like(s)).unsqueeze(-1)
+    a = z.abs()
+    code = sum((a > t if i % 2 == 0 else a >= t).to(torch.uint8)
+               for i, t in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)))
+    return (code | (torch.signbit(z).to(torch.uint8) << 3)).flatten(-2), scale.view(torch.uint8)
+
+
+def fp4_pool(num_slots: int, heads: int, width: int, slots=None, codes=None, scales=None) -> torch.Tensor:
+    """Bytes of a 4-bit pool: rows at `slots`, every other row's scales NaN (and codes 0xF)."""
+    rows = torch.full((num_slots // 16, heads, 16, width // 2), 0xFF, dtype=torch.uint8)
+    sc = torch.full((num_slots // 16, heads, 16, width // 16), E4M3_NAN, dtype=torch.uint8)
+    if slots is not None and len(slots):
+        rows.transpose(1, 2)[slots // 16, slots % 16] = codes[..., 0::2] | (codes[..., 1::2] << 4)
+        sc.transpose(1, 2)[slots // 16, slots % 16] = scales
+    return torch.cat([rows.flatten(2), sc.flatten(2)], -1).contiguous().view(-1)
+
+
+def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0) -> np.ndarray:
+    """fp32 [max_positions, rotary_dim]: cosines, then sines, of position * base^(-2j / rotary_dim)."""
+    angle = np.arange(max_positions)[:, None] * base ** (-np.arange(0, rotary_dim, 2) / rotary_dim)
+    return np.concatenate([np.cos(angle), np.sin(angle)], -1).astype(np.float32)
+
+
+def new_positions(prefix_lens, qo_lens) -> np.ndarray:
+    """Positions of each request's new tokens, in the order of its query rows."""
+    return np.concatenate([np.arange(p, p + n) for p, n in zip(prefix_lens, qo_lens)]
+                          + [np.zeros(0)]).astype(np.int32)
+
+
+def alibi_slopes(num_q_heads: int) -> np.ndarray:
+    """The geometric sequence 2^(-8 (h + 1) / heads), fp32."""
+    return (2.0 ** (-8.0 * np.arange(1, num_q_heads + 1) / num_q_heads)).astype(np.float32)
 
 
 def bf16_bits(t: torch.Tensor) -> np.ndarray:
@@ -195,7 +250,7 @@ def make_workload(name: str, mode: str, bs: int, num_q_heads: int, num_kv_heads:
     q = _randn_bf16(g1, (T, num_q_heads, head_dim))
 
     fp8 = kv_dtype == "fp8_e4m3"
-    if kv_dtype not in ("bf16", "fp8_e4m3"):
+    if kv_dtype not in ("bf16", "fp8_e4m3", "fp4_e2m1"):
         raise ValueError(kv_dtype)
     pools = []
     scales = []
@@ -210,6 +265,12 @@ def make_workload(name: str, mode: str, bs: int, num_q_heads: int, num_kv_heads:
             pool = torch.full((num_slots, num_kv_heads, width), E4M3_NAN, dtype=torch.uint8)
             codes = (data / scale).to(torch.float8_e4m3fn).view(torch.uint8)
             pool[idx] = codes
+        elif kv_dtype == "fp4_e2m1":
+            # the largest value's block scale is the largest E4M3 value
+            amax = float(data.abs().max()) if n_prefix else 1.0
+            scale = float(np.float32(amax / (6.0 * E4M3_MAX))) if amax > 0 else 1.0
+            inv = float(np.float32(1.0) / np.float32(scale))
+            pool = fp4_pool(num_slots, num_kv_heads, width, idx, *fp4_pack_rows(data, inv))
         else:
             scale = 1.0
             pool = torch.full((num_slots, num_kv_heads, width), BF16_NAN, dtype=torch.int16)
