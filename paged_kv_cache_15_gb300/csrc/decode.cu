@@ -27,8 +27,8 @@
 //     the tcgen05 tile kernel of extend.cu walks this path's plan (the same
 //     split items, the same merge below).
 //   * Each unit ends with its normalised output and LSE. A request with one split
-//     writes the final bf16 output directly; otherwise the unit writes a bf16
-//     partial row and an fp32 LSE, and the merge kernel (one warp per
+//     writes the final bf16 output directly; otherwise the unit writes a
+//     partial row (enum PartKind) and an fp32 LSE, and the merge kernel (one warp per
 //     (token, query head) row) combines them:
 //        lse = ln sum_s exp(lse_s),  o = sum_s exp(lse_s - lse) o_s.
 //   * FP8 E4M3 pools: codes are widened to f16 in registers (cvt e4m3x2 -> f16x2,
@@ -54,6 +54,7 @@ template <int DK_, int DV_, int KV_, int WK_, int KPW_, int STAGES_, int RT_>
 struct DecodeCfg {
   static constexpr int DK = DK_;
   static constexpr int DV = DV_;
+  static constexpr int KV = KV_;
   static constexpr bool FP8 = KV_ == PKV_KV_FP8_E4M3;
   static constexpr bool FP4 = KV_ == PKV_KV_FP4_E2M1;
   static constexpr bool F16 = KV_ != PKV_KV_BF16;  // MMAs in f16 (codes widened exactly), else bf16
@@ -89,7 +90,7 @@ struct DecodeCfg {
   static constexpr int kUnitQOffset = kAbortOffset + 16;  // unit queue: 2 full + 2 empty barriers, 2 ids
   static constexpr int kSmemBytes = kUnitQOffset + 40 + 1024;  // + alignment slack
   static_assert(FP4 || (kRowBytesK % 128 == 0 && kRowBytesV % 128 == 0), "rows must be whole 128-byte swizzle spans");
-  static_assert(!FP4 || (DK == 128 && DV == 128 && kStagePages <= 16), "4-bit tiles of 128-wide heads, one lane a copy");
+  static_assert(!FP4 || (DK == 128 && DV == 128 && kStagePages <= 16 && KPW == 32), "4-bit tiles of 128-wide heads, one lane a copy");
   static_assert(KPW % 16 == 0 && kStageKeys % kSegSlots == 0, "stage must hold whole pages");
   static_assert(kOwnScratch || WK * 16 * DV * 4 <= kStageBytes, "merge scratch must fit in one stage");
   static_assert(WK > 1 && RT >= 1 && RT <= 2, "key-major tiles: one or two 8-row tiles, key warps combined");
@@ -153,42 +154,51 @@ __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w &
 // (ld.global.cg), never from a stale L1 line.
 constexpr int kMergeBatch = 8;
 
-template <int D>
-struct MergeVec;
-// partial rows are bf16: 4 (D = 128) or 2 (D = 64) elements per lane
-template <>
-struct MergeVec<128> {
-  using T = uint2;
-  __device__ static T load(const uint16_t* p) { return __ldcg(reinterpret_cast<const uint2*>(p)); }
-  __device__ static void fma(float* acc, float w, const T& x) {
-    acc[0] += w * bf16lo(x.x);
-    acc[1] += w * bf16hi(x.x);
-    acc[2] += w * bf16lo(x.y);
-    acc[3] += w * bf16hi(x.y);
+// A lane's 4 (D = 128) or 2 (D = 64) elements of a partial row (enum PartKind).
+template <int D, int KIND>
+struct MergeVec {
+  static constexpr int N = D / 64;  // element pairs
+  uint32_t w[KIND == kPartF32 ? 2 * N : N];
+  __device__ void load(const uint16_t* rows, long long elem) {
+    const void* p = KIND == kPartF32 ? (const void*)(reinterpret_cast<const float*>(rows) + elem) : rows + elem;
+    if constexpr (KIND == kPartF32 && N == 2) {
+      const uint4 x = __ldcg(static_cast<const uint4*>(p));
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (KIND == kPartF32 || N == 2) {
+      const uint2 x = __ldcg(static_cast<const uint2*>(p));
+      w[0] = x.x, w[1] = x.y;
+    } else {
+      w[0] = __ldcg(static_cast<const unsigned int*>(p));
+    }
   }
-};
-template <>
-struct MergeVec<64> {
-  using T = uint32_t;
-  __device__ static T load(const uint16_t* p) { return __ldcg(reinterpret_cast<const unsigned int*>(p)); }
-  __device__ static void fma(float* acc, float w, const T& x) {
-    acc[0] += w * bf16lo(x);
-    acc[1] += w * bf16hi(x);
+  __device__ void fma(float* acc, float f) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (KIND == kPartF32) {
+        acc[2 * i] += f * __uint_as_float(w[2 * i]);
+        acc[2 * i + 1] += f * __uint_as_float(w[2 * i + 1]);
+      } else if constexpr (KIND == kPartF16) {
+        acc[2 * i] += f * __half2float(__ushort_as_half((unsigned short)(w[i] & 0xffffu)));
+        acc[2 * i + 1] += f * __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
+      } else {
+        acc[2 * i] += f * bf16lo(w[i]);
+        acc[2 * i + 1] += f * bf16hi(w[i]);
+      }
+    }
   }
 };
 
-template <int D>
+template <int D, int KIND>
 __device__ __forceinline__ void merge_row(const DecodeArgs& a, long long pbase, int qo, int i, int h, int nsplit,
                                           long long orow, int lane) {
   constexpr int PER = D / 32;
-  using V = MergeVec<D>;
   auto prow = [&](int sp) { return (pbase + (long long)sp * qo + i) * a.num_q_heads + h; };
   auto lse_of = [&](int sp) { return __ldcg(a.m.partial_lse + prow(sp)); };
-  auto part = [&](int sp) { return V::load(a.m.partial_o + prow(sp) * D + lane * PER); };
-  typename V::T x[kMergeBatch];
+  MergeVec<D, KIND> x[kMergeBatch];
+  auto load = [&](int i, int sp) { x[i].load(a.m.partial_o, prow(sp) * D + lane * PER); };
 #pragma unroll
   for (int sp = 0; sp < kMergeBatch; ++sp)
-    if (sp < nsplit) x[sp] = part(sp);
+    if (sp < nsplit) load(sp, sp);
   static_assert(kMaxSplitsPerRequest <= 64, "two splits per lane");
   const float l0 = lane < nsplit ? lse_of(lane) : -INFINITY;
   const float l1 = lane + 32 < nsplit ? lse_of(lane + 32) : -INFINITY;
@@ -208,18 +218,22 @@ __device__ __forceinline__ void merge_row(const DecodeArgs& a, long long pbase, 
   for (int j = 0; j < PER; ++j) acc[j] = 0.f;
 #pragma unroll
   for (int sp = 0; sp < kMergeBatch; ++sp)
-    if (sp < nsplit) V::fma(acc, weight(sp), x[sp]);
+    if (sp < nsplit) x[sp].fma(acc, weight(sp));
   for (int s0 = kMergeBatch; s0 < nsplit; s0 += kMergeBatch) {
 #pragma unroll
     for (int sp = 0; sp < kMergeBatch; ++sp)
-      if (s0 + sp < nsplit) x[sp] = part(s0 + sp);
+      if (s0 + sp < nsplit) load(sp, s0 + sp);
 #pragma unroll
     for (int sp = 0; sp < kMergeBatch; ++sp) {
       if (s0 + sp >= nsplit) break;
-      V::fma(acc, weight(s0 + sp), x[sp]);
+      x[sp].fma(acc, weight(s0 + sp));
     }
   }
   float lse = Z > 0.f ? M + __logf(Z) : -INFINITY;
+  if constexpr (KIND == kPartF16) {  // rows in units of the codes
+#pragma unroll
+    for (int j = 0; j < PER; ++j) acc[j] *= a.v_scale;
+  }
   if (a.sinks) {
     const float f = sink_factor(lse, a.sinks[h]);
 #pragma unroll
@@ -242,6 +256,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
                                                                      const __grid_constant__ CUtensorMap tmap_v,
                                                                      DecodeArgs a) {
   constexpr int DK = C::DK, DV = C::DV;
+  constexpr int PK = part_kind(C::KV, EXTRAS);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
@@ -583,20 +598,22 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
           named_bar_sync(1, C::kConsumerWarps * 32);
         }
 
-        if (!skip) {
-#pragma unroll
-          for (int kb = 0; kb < C::KPW / 16; ++kb) {
-            const int kr0 = wk * C::KPW + kb * 16;  // first stage row of this 16-key block
-            const int abs0 = stage_key0 + kr0;
-            if (abs0 >= key_end) break;
-            // ---- S^T = K Q^T: s[j] = {(key g8, row 2t4), (g8, 2t4+1), (g8+8, 2t4), (g8+8, 2t4+1)}
-            float s[RT][4];
-#pragma unroll
-            for (int j = 0; j < RT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-            if constexpr (C::FP4) {
-              // lane: 32 codes (two blocks) of key rows g8 and g8 + 8, times
-              // their block scales (exact in f16: at most 6 significant bits)
-              const uint32_t tile = kbase + (kr0 / kSegSlots) * fp4_tile_bytes(DK);
+        if constexpr (C::FP4) {
+          // One online-softmax step over the warp's two 16-key blocks. The
+          // running maximum moves only when a score passes it by more than
+          // kSlack (p then stays at most 2^kSlack, well inside f16), so most
+          // steps need one warp vote and no exchange between lanes.
+          constexpr float kSlack = 8.f;
+          const int kr0 = wk * C::KPW, abs0 = stage_key0 + kr0;
+          if (!skip && abs0 < key_end) {
+            const bool two = abs0 + 16 < key_end;
+            const float scale = EXTRAS == kExtrasScores ? 1.f : a.scale_log2;
+            // S^T = K Q^T of block kb. Lane: 32 codes (two blocks of columns) of
+            // key rows g8 and g8 + 8, times their block scales (exact in f16: at
+            // most 6 significant bits)
+            float s[2][RT][4];
+            auto scores = [&](int kb) {
+              const uint32_t tile = kbase + (kr0 / kSegSlots + kb) * fp4_tile_bytes(DK);
               uint32_t kf[2][16];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
@@ -613,12 +630,143 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
                 for (int i = 0; i < 16; ++i) kf[h][i] = mul_f16x2(kf[h][i], i < 8 ? s0 : s1);
               }
 #pragma unroll
+              for (int j = 0; j < RT; ++j) s[kb][j][0] = s[kb][j][1] = s[kb][j][2] = s[kb][j][3] = 0.f;
+#pragma unroll
               for (int kk = 0; kk < DK / 16; ++kk) {
                 const uint32_t ka[4] = {kf[0][2 * kk], kf[1][2 * kk], kf[0][2 * kk + 1], kf[1][2 * kk + 1]};
 #pragma unroll
-                for (int j = 0; j < RT; ++j) mma_f16(s[j], ka, qf[kk][j][0], qf[kk][j][1]);
+                for (int j = 0; j < RT; ++j) mma_f16(s[kb][j], ka, qf[kk][j][0], qf[kk][j][1]);
               }
-            } else if constexpr (!C::FP8) {
+            };
+            scores(0);
+            if (two) {
+              scores(1);
+            } else {
+#pragma unroll
+              for (int j = 0; j < RT; ++j) s[1][j][0] = s[1][j][1] = s[1][j][2] = s[1][j][3] = -INFINITY;
+            }
+            // score changes and masks; steps that every row sees whole skip them
+            const bool whole = EXTRAS != kExtrasScores && abs0 + 31 < key_end && abs0 + 31 <= prefix &&
+                               !(tree && abs0 + 31 >= prefix);
+            if (!whole) {
+#pragma unroll
+              for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int j = 0; j < RT; ++j)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * j + 2 * t4 + e;
+                    const uint64_t tw =
+                        tree && abs0 + 31 >= prefix && r < rows_valid ? tree_words[q0 + r / G] : ~0ull;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                      const int kp = abs0 + 16 * kb + krow + 8 * h;
+                      float& x = s[kb][j][2 * h + e];
+                      if constexpr (EXTRAS == kExtrasScores)
+                        x = (a.mods.cap2 != 0.f ? capped_score(a.mods, x) : x * a.scale_log2) +
+                            slope[j][e] * (float)(kp - lim[j][e]);
+                      bool ok = kp < key_end && kp <= lim[j][e];
+                      if (tree && kp >= prefix) ok = ok && kp - prefix < 64 && ((tw >> (kp - prefix)) & 1ull);
+                      x = ok ? x : -INFINITY;
+                    }
+                  }
+            }
+            bool grow = false;
+            float top[RT][2];
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                top[j][e] = fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e])) * scale;
+                grow |= top[j][e] > m[j][e] + kSlack;
+              }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+              for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float mx = top[j][e];
+                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                  const float mn = fmaxf(m[j][e], mx);
+                  const float al = mn == -INFINITY ? 1.f : fast_exp2(m[j][e] - mn);
+                  m[j][e] = mn;
+                  l[j][e] *= al;
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) {
+                    o[mt][j][e] *= al;
+                    o[mt][j][2 + e] *= al;
+                  }
+                }
+            }
+            uint32_t pb[2][RT][2];
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float ref = m[j][e] == -INFINITY ? 0.f : m[j][e];
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    s[kb][j][2 * h + e] = fast_exp2(fmaf(s[kb][j][2 * h + e], scale, -ref));
+                l[j][e] += (s[0][j][e] + s[0][j][2 + e]) + (s[1][j][e] + s[1][j][2 + e]);
+              }
+              // P^T as the B operand: the accumulator layout of keys 0-7 and 8-15
+              // is that of an ldmatrix fragment, and its transpose is B's
+#pragma unroll
+              for (int kb = 0; kb < 2; ++kb) {
+                pb[kb][j][0] = movmatrix_trans(pack_f16(s[kb][j][0], s[kb][j][1]));
+                pb[kb][j][1] = movmatrix_trans(pack_f16(s[kb][j][2], s[kb][j][3]));
+              }
+            }
+            // O^T += V^T P^T. Lane: the 16 codes of block g8 (columns 16g ..
+            // 16g + 15) of its four keys; m-row g8 of m-tile mt is column 16g +
+            // 2mt, m-row g8 + 8 the next. Two keys' codes of a column are brought
+            // together in one byte, so a conversion gives the A register's key pair.
+            auto values = [&](int kb) {
+              const uint32_t tile = vbase + (kr0 / kSegSlots + kb) * fp4_tile_bytes(DV);
+              uint32_t vf[2][2][8];  // [key half][column parity][mt]
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int k0 = fp4_key(2 * t4) + 8 * h, k1 = fp4_key(2 * t4 + 1) + 8 * h;
+                const uint2 x = lds_v2(tile + k0 * (DV / 2) + 8 * g8), y = lds_v2(tile + k1 * (DV / 2) + 8 * g8);
+                const uint32_t scales = tile + kSegSlots * (DV / 2) + g8;
+                const uint32_t sc = e4m3x2_to_f16x2(
+                    (uint16_t)(lds_u8(scales + k0 * (DV / 16)) | (lds_u8(scales + k1 * (DV / 16)) << 8)));
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                e2m1x8_to_f16x2((x.x & kLow) | ((y.x << 4) & ~kLow), vf[h][0]);
+                e2m1x8_to_f16x2((x.y & kLow) | ((y.y << 4) & ~kLow), vf[h][0] + 4);
+                e2m1x8_to_f16x2(((x.x >> 4) & kLow) | (y.x & ~kLow), vf[h][1]);
+                e2m1x8_to_f16x2(((x.y >> 4) & kLow) | (y.y & ~kLow), vf[h][1] + 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  vf[h][0][i] = mul_f16x2(vf[h][0][i], sc);
+                  vf[h][1][i] = mul_f16x2(vf[h][1][i], sc);
+                }
+              }
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                const uint32_t va[4] = {vf[0][0][mt], vf[0][1][mt], vf[1][0][mt], vf[1][1][mt]};
+#pragma unroll
+                for (int j = 0; j < RT; ++j) mma_f16(o[mt][j], va, pb[kb][j][0], pb[kb][j][1]);
+              }
+            };
+            values(0);
+            if (two) values(1);
+          }
+        } else if (!skip) {
+#pragma unroll
+          for (int kb = 0; kb < C::KPW / 16; ++kb) {
+            const int kr0 = wk * C::KPW + kb * 16;  // first stage row of this 16-key block
+            const int abs0 = stage_key0 + kr0;
+            if (abs0 >= key_end) break;
+            // ---- S^T = K Q^T: s[j] = {(key g8, row 2t4), (g8, 2t4+1), (g8+8, 2t4), (g8+8, 2t4+1)}
+            float s[RT][4];
+#pragma unroll
+            for (int j = 0; j < RT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+            if constexpr (!C::FP8) {
               const int key = kr0 + (lane & 15);
 #pragma unroll
               for (int kk = 0; kk < DK / 16; ++kk) {
@@ -731,38 +879,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
               pb[j][1] = movmatrix_trans(C::F16 ? pack_f16(s[j][2], s[j][3]) : pack_bf16(s[j][2], s[j][3]));
             }
             // ---- O^T += V^T P^T ----
-            if constexpr (C::FP4) {
-              // lane: the 16 codes of block g8 (columns 16g .. 16g + 15) of its
-              // four keys; m-row g8 of m-tile mt is column 16g + 2mt, m-row g8 + 8
-              // the next. Two keys' codes of a column are brought together in one
-              // byte, so a conversion gives the A register's key pair.
-              const uint32_t tile = vbase + (kr0 / kSegSlots) * fp4_tile_bytes(DV);
-              uint32_t vf[2][2][8];  // [key half][column parity][mt]
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int k0 = fp4_key(2 * t4) + 8 * h, k1 = fp4_key(2 * t4 + 1) + 8 * h;
-                const uint2 x = lds_v2(tile + k0 * (DV / 2) + 8 * g8), y = lds_v2(tile + k1 * (DV / 2) + 8 * g8);
-                const uint32_t scales = tile + kSegSlots * (DV / 2) + g8;
-                const uint32_t sc = e4m3x2_to_f16x2(
-                    (uint16_t)(lds_u8(scales + k0 * (DV / 16)) | (lds_u8(scales + k1 * (DV / 16)) << 8)));
-                constexpr uint32_t kLow = 0x0f0f0f0fu;
-                e2m1x8_to_f16x2((x.x & kLow) | ((y.x << 4) & ~kLow), vf[h][0]);
-                e2m1x8_to_f16x2((x.y & kLow) | ((y.y << 4) & ~kLow), vf[h][0] + 4);
-                e2m1x8_to_f16x2(((x.x >> 4) & kLow) | (y.x & ~kLow), vf[h][1]);
-                e2m1x8_to_f16x2(((x.y >> 4) & kLow) | (y.y & ~kLow), vf[h][1] + 4);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  vf[h][0][i] = mul_f16x2(vf[h][0][i], sc);
-                  vf[h][1][i] = mul_f16x2(vf[h][1][i], sc);
-                }
-              }
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                const uint32_t va[4] = {vf[0][0][mt], vf[0][1][mt], vf[1][0][mt], vf[1][1][mt]};
-#pragma unroll
-                for (int j = 0; j < RT; ++j) mma_f16(o[mt][j], va, pb[j][0], pb[j][1]);
-              }
-            } else if constexpr (!C::FP8) {
+            if constexpr (!C::FP8) {
               const int key = kr0 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
@@ -831,7 +948,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
           lrow = a.lse ? a.lse + t * a.num_q_heads + h : nullptr;
         } else {
           const long long pr = (long long)a.m.partial_indptr[b] + (long long)split * qo + i;
-          orow = a.m.partial_o + (pr * a.num_q_heads + h) * DV;
+          orow = a.m.partial_o + (pr * a.num_q_heads + h) * DV * (PK == kPartF32 ? 2 : 1);
           lrow = a.m.partial_lse + pr * a.num_q_heads + h;
         }
       };
@@ -849,7 +966,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
             uint16_t* orow;
             float* lrow;
             out_row(r, orow, lrow);
-            *reinterpret_cast<uint32_t*>(orow + 2 * c2) = 0u;
+            if (PK == kPartF32 && !direct)
+              *reinterpret_cast<uint2*>(orow + 4 * c2) = make_uint2(0u, 0u);
+            else
+              *reinterpret_cast<uint32_t*>(orow + 2 * c2) = 0u;
             // no key: the LSE is the sink's alone (final rows only)
             if (c2 == 0 && lrow) *lrow = (direct && sinks) ? sinks[g * G + r % G] : -INFINITY;
           }
@@ -905,7 +1025,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
             wgt[k] = (M == -INFINITY) ? 0.f : fast_exp2(mw[k] - M);
             Lsum += lw[k] * wgt[k];
           }
-          const float inv = Lsum > 0.f ? a.v_scale / Lsum : 0.f;
+          // (f16 partial rows stay in units of the codes)
+          const float inv = Lsum > 0.f ? (PK == kPartF16 && !direct ? 1.f : a.v_scale) / Lsum : 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < C::WK; ++k) {
@@ -928,8 +1049,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
           uint16_t* orow;
           float* lrow;
           out_row(r, orow, lrow);
-          *reinterpret_cast<uint2*>(orow + c4 * 4) = make_uint2(pack_bf16(acc.x * inv * fs, acc.y * inv * fs),
-                                                                pack_bf16(acc.z * inv * fs, acc.w * inv * fs));
+          if (PK == kPartF32 && !direct)
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(orow) + c4 * 4) =
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          else if (PK == kPartF16 && !direct)
+            *reinterpret_cast<uint2*>(orow + c4 * 4) =
+                make_uint2(pack_f16(acc.x * inv, acc.y * inv), pack_f16(acc.z * inv, acc.w * inv));
+          else
+            *reinterpret_cast<uint2*>(orow + c4 * 4) = make_uint2(pack_bf16(acc.x * inv * fs, acc.y * inv * fs),
+                                                                  pack_bf16(acc.z * inv * fs, acc.w * inv * fs));
           if (c4 == 0 && lrow) *lrow = lse_r;
         }
         if constexpr (!C::kOwnScratch) {
@@ -957,7 +1085,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
 // counts, the decode path the decode plan's.
 // One warp per (token, query head) row of the batch; rows of requests that
 // were not split on this path are skipped.
-template <int D>
+template <int D, int KIND>
 __global__ void __launch_bounds__(256, 3) split_merge_kernel(DecodeArgs a, int max_rows_per_head, int count_word,
                                                           int extend_path) {
   pdl_wait();  // the partial rows come from the preceding attention grid
@@ -985,7 +1113,7 @@ __global__ void __launch_bounds__(256, 3) split_merge_kernel(DecodeArgs a, int m
       pbase = a.m.partial_indptr[b];
     }
     if (nsplit <= 1 || qo * a.group > max_rows_per_head) continue;
-    merge_row<D>(a, pbase, qo, t - q0, h, nsplit, (long long)row, lane);
+    merge_row<D, KIND>(a, pbase, qo, t - q0, h, nsplit, (long long)row, lane);
   }
 }
 
@@ -1025,14 +1153,15 @@ int run_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   a.mods = score_mods(c, a.scale_log2);
   a.k_pool = static_cast<const uint8_t*>(k_pool);
   a.v_pool = static_cast<const uint8_t*>(v_pool);
-  auto kernel = a.mods.cap2 > 0.f || a.mods.slopes ? decode_splitkv_kernel<C, kExtrasScores>
-                : a.tree || a.sinks                ? decode_splitkv_kernel<C, kExtrasMask>
-                                                   : decode_splitkv_kernel<C, kExtrasNone>;
+  const int extras = extras_of(c);
+  auto kernel = extras == kExtrasScores ? decode_splitkv_kernel<C, kExtrasScores>
+                : extras == kExtrasMask ? decode_splitkv_kernel<C, kExtrasMask>
+                                        : decode_splitkv_kernel<C, kExtrasNone>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
     return PKV_ERR_CUDA;
   if (launch_pdl(kernel, dim3(c.decode_ctas), dim3(C::kThreads), C::kSmemBytes, st, tk, tv, a) != cudaSuccess)
     return PKV_ERR_CUDA;
-  return launch_split_merge(c, out, lse, c.cfg.max_qo_len * a.group, false, st);
+  return launch_split_merge(c, out, lse, a.v_scale, c.cfg.max_qo_len * a.group, false, st);
 }
 
 // Tile shapes: one or two 8-row key-major tiles per unit; four key warps
@@ -1104,7 +1233,8 @@ int launch_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool,
   return PKV_ERR_UNSUPPORTED;
 }
 
-int launch_split_merge(Ctx& c, void* out, float* lse, int max_rows_per_head, bool extend_path, cudaStream_t st) {
+int launch_split_merge(Ctx& c, void* out, float* lse, float v_scale, int max_rows_per_head, bool extend_path,
+                       cudaStream_t st) {
   DecodeArgs a;
   a.m = make_meta(c);
   a.q = nullptr;
@@ -1114,7 +1244,7 @@ int launch_split_merge(Ctx& c, void* out, float* lse, int max_rows_per_head, boo
   a.num_kv_heads = c.cfg.num_kv_heads;
   a.group = c.cfg.num_q_heads / c.cfg.num_kv_heads;
   a.scale_log2 = 0.f;
-  a.v_scale = 1.f;
+  a.v_scale = v_scale;
   a.tree = nullptr;
   a.sinks = c.sinks;
   a.mods = ScoreMods{};  // the merge combines finished partial rows
@@ -1126,12 +1256,13 @@ int launch_split_merge(Ctx& c, void* out, float* lse, int max_rows_per_head, boo
   const int word = extend_path ? kSplitExtend : kSplitDecode;
   cudaError_t e;
   // partial and output rows have the V heads' width
-  if (head_dim_v(c.cfg) == 128)
-    e = launch_pdl(split_merge_kernel<128>, dim3((unsigned)grid), dim3(256), 0, st, a, max_rows_per_head, word,
-                   extend_path ? 1 : 0);
-  else
-    e = launch_pdl(split_merge_kernel<64>, dim3((unsigned)grid), dim3(256), 0, st, a, max_rows_per_head, word,
-                   extend_path ? 1 : 0);
+  const int kind = part_kind(c.cfg.kv_dtype, extras_of(c));
+  auto kernel = head_dim_v(c.cfg) == 128 ? (kind == kPartBf16  ? split_merge_kernel<128, kPartBf16>
+                                            : kind == kPartF16 ? split_merge_kernel<128, kPartF16>
+                                                               : split_merge_kernel<128, kPartF32>)
+                : kind == kPartBf16      ? split_merge_kernel<64, kPartBf16>
+                                         : split_merge_kernel<64, kPartF32>;  // (coded pools: 128-wide heads)
+  e = launch_pdl(kernel, dim3((unsigned)grid), dim3(256), 0, st, a, max_rows_per_head, word, extend_path ? 1 : 0);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

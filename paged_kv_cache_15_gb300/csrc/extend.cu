@@ -164,24 +164,34 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8(const uint4& v) {
 // tile A the first half of the KV range, tile B the rest) streams, for each
 // step j, tile A's tile and then tile B's. Producers, MMA warp and softmax
 // warps all walk this same sequence.
+//
+// rev: the same tiles from the far end of each range to its start (batches with
+// a distance bias, see the softmax role). Tile X's j-th KV tile is then its
+// (n - 1 - j)-th, and a shared unit streams kv0 + len - 1 - j; the tile with the
+// shorter range joins late instead of leaving early (off).
 struct UnitKV {
   int s0, s1, n0, n1;  // tile A's and tile B's KV tiles: [s0, s0 + n0), [s1, s1 + n1)
-  bool dual;
+  bool dual, rev;
   __device__ __forceinline__ int start(int x) const { return x == 0 ? s0 : s1; }
   __device__ __forceinline__ int n(int x) const { return x == 0 ? n0 : n1; }
   __device__ __forceinline__ int steps() const { return max(n0, n1); }
   __device__ __forceinline__ int len() const { return dual ? n0 + n1 : max(n0, n1); }
   // position in the unit's ring sequence of tile X's j-th KV tile
   __device__ __forceinline__ int pos(int x, int j) const {
-    if (!dual) return j;
+    if (!dual) return off(x) + j;
     return x == 0 ? j + min(j, n1) : j + min(j + 1, n0);
   }
+  // tile X's j-th KV tile
+  __device__ __forceinline__ int tile(int x, int j) const { return start(x) + (rev ? n(x) - 1 - j : j); }
+  // first step of a shared unit's ring sequence in which tile X takes part
+  __device__ __forceinline__ int off(int x) const { return rev ? len() - n(x) : 0; }
   // tile X's QKs read Q tile X (a dual unit's tiles both read Q tile A)
   __device__ __forceinline__ bool uses_q(int x) const { return dual ? x == 0 : n(x) > 0; }
 };
 
-__device__ __forceinline__ UnitKV unit_kv(const ExtendTile& u) {
+__device__ __forceinline__ UnitKV unit_kv(const ExtendTile& u, bool rev) {
   UnitKV k;
+  k.rev = rev;
   k.dual = u.dual != 0;
   if (k.dual) {
     const int n = max(0, min(u.kv1, u.kv_a) - u.kv0);
@@ -209,6 +219,7 @@ struct ExtCfg {
   static constexpr int DV = DV_;
   static constexpr int NK = NK_;  // K ring depth
   static constexpr int NV = NV_;  // V ring depth
+  static constexpr int KV = KV_;
   static constexpr bool FP4 = KV_ == PKV_KV_FP4_E2M1;
   static constexpr bool CODED = KV_ != PKV_KV_BF16;  // E4M3 or 4-bit: f16 operands widened from codes
   static constexpr int RK = RK_;  // raw K tiles in flight
@@ -295,6 +306,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
                                                                    ExtendArgs a) {
   constexpr int DK = C::DK, DV = C::DV;
   constexpr int NK = C::NK, NV = C::NV;
+  constexpr int PK = part_kind(C::KV, EXTRAS);
   constexpr int kPagesPerTile = kExtendKeys / kSegSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -370,6 +382,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
   // Tile X of unit u takes its Q by TMA when the box of 128/G tokens lies
   // inside the batch's tokens (never past the end of the caller's q buffer);
   // otherwise the softmax warps write it.
+  // distance bias: KV tiles from the nearest to the farthest
+  const bool rev = EXTRAS == kExtrasScores && a.mods.slopes != nullptr;
   auto q_by_tma = [&](const ExtendTile& u, int x) {
     return a.q_tma != 0 && a.m.qo_indptr[u.b] + (u.row0 + x * kExtendRows) / G + a.q_box_tokens <= total_q;
   };
@@ -409,17 +423,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
     for (int w = blockIdx.x; w < n_units && !stop; w += gridDim.x) {
       const ExtendTile u = load_unit(a, w / a.num_kv_heads);
       const int g = w % a.num_kv_heads;
-      const UnitKV ukv = unit_kv(u);
+      const UnitKV ukv = unit_kv(u, rev);
       const int np = a.m.seg_indptr[u.b + 1] - a.m.seg_indptr[u.b];
       const int page_base = a.m.seg_indptr[u.b];
       const bool reused = !a.dplan && (a.m.qo_indptr[u.b + 1] - a.m.qo_indptr[u.b]) * G > kExtendUnitRows;
       const uint64_t pol = reused ? pol_reuse : pol_stream;
       auto seq_tile = [&](int e) {
-        if (!ukv.dual) return ukv.s0 + e;
+        if (!ukv.dual) return ukv.s0 + (rev ? ukv.len() - 1 - e : e);
         const int m = min(ukv.n0, ukv.n1);
         const int step = e < 2 * m ? e >> 1 : e - m;
         const int x = e < 2 * m ? (e & 1) : (ukv.n0 > ukv.n1 ? 0 : 1);
-        return ukv.start(x) + step;
+        return ukv.tile(x, step);
       };
       const int len = ukv.len();
       // page indices of 4 consecutive tiles: lane 8k + p holds page p of tile e0 + k
@@ -601,7 +615,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
     for (int w = blockIdx.x; w < n_units && !stop; w += gridDim.x) {
       const ExtendTile u = load_unit(a, w / a.num_kv_heads);
       const int g = w % a.num_kv_heads;
-      const UnitKV ukv = unit_kv(u);
+      const UnitKV ukv = unit_kv(u, rev);
       const int np = a.m.seg_indptr[u.b + 1] - a.m.seg_indptr[u.b];
       const int page_base = a.m.seg_indptr[u.b];
       const bool reused = !a.dplan && (a.m.qo_indptr[u.b + 1] - a.m.qo_indptr[u.b]) * G > kExtendUnitRows;
@@ -642,11 +656,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
       }
       // e-th KV tile of the unit's sequence
       auto seq_tile = [&](int e) {
-        if (!ukv.dual) return ukv.s0 + e;
+        if (!ukv.dual) return ukv.s0 + (rev ? ukv.len() - 1 - e : e);
         const int m = min(ukv.n0, ukv.n1);
         const int step = e < 2 * m ? e >> 1 : e - m;
         const int x = e < 2 * m ? (e & 1) : (ukv.n0 > ukv.n1 ? 0 : 1);
-        return ukv.start(x) + step;
+        return ukv.tile(x, step);
       };
       // page indices of 4 consecutive tiles of the sequence: lane 8k + p holds
       // page p of tile e0 + k; the next group is loaded while this one is used
@@ -742,7 +756,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
     };
     for (int w = blockIdx.x; w < n_units && ok; w += gridDim.x) {
       const ExtendTile u = load_unit(a, w / a.num_kv_heads);
-      const UnitKV ukv = unit_kv(u);
+      const UnitKV ukv = unit_kv(u, rev);
       const int n[2] = {ukv.n0, ukv.n1};
       const int nT = ukv.steps();
       if (nT == 0) continue;
@@ -755,8 +769,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         // prologue: S_X of the first tile for both tiles
         if (!wait(&k_full[kt % NK], (kt / NK) & 1)) break;
         tc_fence_after();
+        // tile X takes part in steps [off, end) of the unit's ring sequence
+        const int off[2] = {ukv.off(0), ukv.off(1)};
+        const int end[2] = {off[0] + n[0], off[1] + n[1]};
         for (int x = 0; x < 2; ++x) {
-          if (n[x] == 0) continue;
+          if (n[x] == 0 || off[x] != 0) continue;
           issue_qk(x, x, kt % NK);
           if (n[x] == 1) umma_commit_warp(&q_empty[x]);  // the unit's last QK_X: Q_X may be refilled
         }
@@ -766,26 +783,28 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
           const int vs = vt % NV;
           bool v_ready = false, k_ready = false;
           for (int x = 0; x < 2; ++x) {
-            if (j >= n[x]) continue;
-            if (!wait(&p_full[x], tcount[x] & 1)) break;
-            if (!v_ready) {
-              if (!wait(&v_full[vs], (vt / NV) & 1)) break;
-              v_ready = true;
+            if (j >= end[x]) continue;
+            if (j >= off[x]) {
+              if (!wait(&p_full[x], tcount[x] & 1)) break;
+              if (!v_ready) {
+                if (!wait(&v_full[vs], (vt / NV) & 1)) break;
+                v_ready = true;
+              }
+              // The unit's first PV_X overwrites O_X. The previous unit's epilogue
+              // has read it: the softmax warps release p_full of this tile only
+              // after finishing that epilogue.
+              tc_fence_after();
+              issue_pv(x, vs, j == off[x], j + 1 == end[x]);
+              ++tcount[x];
             }
-            // The unit's first PV_X overwrites O_X. The previous unit's epilogue
-            // has read it: the softmax warps release p_full of this tile only
-            // after finishing that epilogue.
-            tc_fence_after();
-            issue_pv(x, vs, j == 0, j + 1 == n[x]);
-            ++tcount[x];
-            if (j + 1 < n[x]) {
+            if (j + 1 >= off[x] && j + 1 < end[x]) {
               if (!k_ready) {
                 if (!wait(&k_full[kt % NK], (kt / NK) & 1)) break;
                 tc_fence_after();
                 k_ready = true;
               }
               issue_qk(x, x, kt % NK);
-              if (j + 2 == n[x]) umma_commit_warp(&q_empty[x]);  // the unit's last QK_X
+              if (j + 2 == end[x]) umma_commit_warp(&q_empty[x]);  // the unit's last QK_X
             }
           }
           if (!ok) break;
@@ -850,7 +869,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
     for (int w = blockIdx.x; w < n_units && !*s_abort; w += gridDim.x) {
       const ExtendTile u = load_unit(a, w / a.num_kv_heads);
       const int g = w % a.num_kv_heads;
-      const UnitKV ukv = unit_kv(u);
+      const UnitKV ukv = unit_kv(u, rev);
       const int kb = ukv.start(x);  // this tile's KV tiles: [kb, kb + nX)
       const int nX = ukv.n(x);
       const int nA = ukv.n0;
@@ -904,8 +923,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
           }
         } else if (valid) {
           if (split) {
-            for (int c = 0; c < DV; c += 8)
-              *reinterpret_cast<uint4*>(a.m.partial_o + prow * DV + c) = make_uint4(0, 0, 0, 0);
+            constexpr int kHalves = PK == kPartF32 ? 2 * DV : DV;  // 16-bit units of a partial row
+            for (int c = 0; c < kHalves; c += 8)
+              *reinterpret_cast<uint4*>(a.m.partial_o + prow * kHalves + c) = make_uint4(0, 0, 0, 0);
             a.m.partial_lse[prow] = -INFINITY;
           } else {
             for (int c = 0; c < DV; c += 8)
@@ -941,7 +961,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
       float m_ref = 0.f, l = 0.f;
       bool aborted = false;
       for (int jr = 0; jr < nX; ++jr) {
-        const int j = kb + jr;                      // absolute KV tile
+        const int j = ukv.tile(x, jr);              // absolute KV tile
         const uint32_t jj = jt + ukv.pos(x, jr);    // its place in the V ring sequence
         // warp-uniform waits: every lane of the warp leaves the loop together
         if (!mbar_wait_warp(&s_full[x], tcount & 1, plan, s_abort)) {
@@ -950,13 +970,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         }
         tc_fence_after();
         const int key0 = j * kExtendKeys;
+        // (With a distance bias the tiles come nearest first: a steep head's
+        // scores fall by slope * 128 a tile, so its first tile sets the reference
+        // and the later ones stay below it, instead of each outgrowing the last.)
         // some keys of this tile are masked for this row: past its limit, or
         // drafts that its tree may hide
         const bool diag =
             key0 + kExtendKeys - 1 > limit || (EXTRAS != kExtrasNone && key0 + kExtendKeys > draft0);
         // the request's last page inside this KV tile: zero the V rows past L
         // (done by the first tile that reads this V tile, before its PV)
-        if ((ukv.dual || x == 0 || jr >= nA) && np <= (j + 1) * kPagesPerTile && (L % kSegSlots) != 0) {
+        if ((ukv.dual || x == 0 || j - kb >= nA) && np <= (j + 1) * kPagesPerTile && (L % kSegSlots) != 0) {
           const int vs = jj % NV;
           if (!mbar_wait_warp(&v_full[vs], (jj / NV) & 1, plan, s_abort)) {
             aborted = true;
@@ -1121,7 +1144,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         m_ref = m;
       }
       float inv = l > 0.f ? 1.f / l : 0.f;
-      if constexpr (C::CODED) inv *= a.v_scale;  // V codes times the pool's scale
+      // V codes times the pool's scale (f16 partial rows stay in units of the codes)
+      if constexpr (C::CODED) inv *= PK == kPartF16 && split ? 1.f : a.v_scale;
       if constexpr (EXTRAS != kExtrasNone) {
         // final rows of a model with sinks: the head's sink joins the normaliser
         if (!split && valid && a.sinks) {
@@ -1160,8 +1184,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
           // the output row, or (split units) a bf16 partial row of the same layout
           uint32_t v[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-          {
+          for (int i = 0; i < 16; ++i) {
+            const float lo = __uint_as_float(o[2 * i]), hi = __uint_as_float(o[2 * i + 1]);
+            v[i] = PK == kPartF16 && split ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+          }
+          if (PK == kPartF32 && split) {
+            float* dst = reinterpret_cast<float*>(a.m.partial_o) + prow * DV + c * 32;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) st_global_32B(dst + i, o + i);
+          } else {
             uint16_t* dst = split ? a.m.partial_o + prow * DV + c * 32 : a.out + orow * DV + c * 32;
             if (split || a.out_32B) {
               st_global_32B(dst, v);
@@ -1264,9 +1295,10 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
     a.q_tma = 1;
     a.q_box_tokens = (int)box_tok;
   }
-  auto kernel = a.mods.cap2 > 0.f || a.mods.slopes ? extend_tc_kernel<C, kExtrasScores>
-                : a.tree || a.sinks                ? extend_tc_kernel<C, kExtrasMask>
-                                                   : extend_tc_kernel<C, kExtrasNone>;
+  const int extras = extras_of(c);
+  auto kernel = extras == kExtrasScores ? extend_tc_kernel<C, kExtrasScores>
+                : extras == kExtrasMask ? extend_tc_kernel<C, kExtrasMask>
+                                        : extend_tc_kernel<C, kExtrasNone>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
     return PKV_ERR_CUDA;
   if (launch_pdl(kernel, dim3(c.extend_ctas), dim3(C::kThreads), C::kSmemBytes, st, tk, tv, tq, a) != cudaSuccess)
@@ -1274,8 +1306,8 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   // the decode plan's split requests are merged by the decode path's merge
   // (its split counts); on the extend path, the requests whose rows fit one
   // unit were split along their KV range
-  if (dplan) return launch_split_merge(c, out, lse, c.cfg.max_qo_len * a.group, false, st);
-  return launch_split_merge(c, out, lse, kExtendUnitRows, true, st);
+  if (dplan) return launch_split_merge(c, out, lse, a.v_scale, c.cfg.max_qo_len * a.group, false, st);
+  return launch_split_merge(c, out, lse, a.v_scale, kExtendUnitRows, true, st);
 }
 
 int run_tc(Ctx& c, const void* q, const void* k_pool, const void* v_pool, float sm_scale, float k_scale,

@@ -75,7 +75,10 @@ void grid_sizes(const pkv_config& cfg, int num_sms, int* decode_ctas, int* exten
   if (*extend_ctas < 1) *extend_ctas = 1;
 }
 
-Layout make_layout(const pkv_config& cfg, int num_sms) {
+// part_bytes: bytes of a partial output element. Contexts hold 4 (score
+// changes on bf16 pools write fp32 rows, enum PartKind); the static decode
+// entry, which has no score changes, 2.
+Layout make_layout(const pkv_config& cfg, int num_sms, size_t part_bytes = sizeof(float)) {
   Layout L;
   int dctas, ectas;
   grid_sizes(cfg, num_sms, &dctas, &ectas);
@@ -109,7 +112,7 @@ Layout make_layout(const pkv_config& cfg, int num_sms) {
   L.seg_indices = L.seg_per_page > 1 ? take(sizeof(int) * (size_t)max_segments(cfg)) : L.kv_indices;
   L.decode_items = take(sizeof(DecodeItem) * (size_t)L.max_decode_items);
   L.extend_tiles = take(sizeof(ExtendTile) * (size_t)L.max_extend_tiles);
-  L.partial_o = take(sizeof(uint16_t) * (size_t)cap * cfg.num_q_heads * head_dim_v(cfg));
+  L.partial_o = take(part_bytes * (size_t)cap * cfg.num_q_heads * head_dim_v(cfg));
   L.partial_lse = take(sizeof(float) * (size_t)cap * cfg.num_q_heads);
   L.total = off;
   return L;
@@ -214,7 +217,7 @@ int encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, void* base, uint
 int static_config_ok(const pkv_config* cfg) { return check_config(cfg); }
 
 size_t static_layout_bytes(const pkv_config& cfg, int num_sms, Layout* lay) {
-  *lay = make_layout(cfg, num_sms);
+  *lay = make_layout(cfg, num_sms, sizeof(uint16_t));
   return lay->total;
 }
 

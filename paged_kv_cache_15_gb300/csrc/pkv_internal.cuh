@@ -124,6 +124,25 @@ inline const uint64_t* active_tree(const Ctx& c) {
 // run without the code of the features they do not use.
 enum Extras : int { kExtrasNone = 0, kExtrasMask = 1, kExtrasScores = 2 };  // 1: tree or sinks, 2: score changes too
 
+// How split units hand their normalised output rows to the merge:
+//   bf16: bf16 and E4M3 pools without score changes;
+//   f16 in units of the codes (before the V pool's scale, so at most 2,688):
+//     4-bit pools, and E4M3 pools with score changes; 8 times finer than bf16
+//     in the same bytes;
+//   fp32: bf16 pools with score changes (their values have no bound that f16
+//     could count on).
+// A bf16 partial row costs as much precision as the rounding of the output
+// itself (its error does not average out over the splits: relative error
+// against 64 bits 0.0024 with it and 0.0017 without, 64 requests of 1,024 to
+// 8,192 keys); the first kind keeps it because its results are fixed.
+enum PartKind : int { kPartBf16 = 0, kPartF16 = 1, kPartF32 = 2 };
+__host__ __device__ constexpr int part_kind(int kv_dtype, int extras) {
+  return kv_dtype == PKV_KV_FP4_E2M1   ? kPartF16
+         : extras != kExtrasScores     ? kPartBf16
+         : kv_dtype == PKV_KV_FP8_E4M3 ? kPartF16
+                                       : kPartF32;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -147,6 +166,11 @@ inline ScoreMods score_mods(const Ctx& c, float scale_log2) {
   return m;
 }
 
+// The instantiation a forward of this context takes.
+inline int extras_of(const Ctx& c) {
+  return c.logit_cap > 0.f || c.slopes ? kExtrasScores : active_tree(c) || c.sinks ? kExtrasMask : kExtrasNone;
+}
+
 // Device-side view of the metadata in the workspace.
 struct Meta {
   int* plan;
@@ -163,7 +187,7 @@ struct Meta {
   const int* token_req;
   const DecodeItem* decode_items;
   const ExtendTile* extend_tiles;
-  uint16_t* partial_o;  // bf16 [rows][Hq][Dv]: normalised partial outputs of split units
+  uint16_t* partial_o;  // [rows][Hq][Dv]: normalised partial outputs of split units (enum PartKind)
   float* partial_lse;
 };
 
@@ -196,7 +220,8 @@ int launch_decode_tc(Ctx& c, const void* q, const void* k_pool, const void* v_po
 // LSE merge of split partials for requests whose rows per KV head are at most
 // max_rows_per_head (the decode path: its largest tile; the extend path: 256,
 // the requests it split).
-int launch_split_merge(Ctx& c, void* out, float* lse, int max_rows_per_head, bool extend_path, cudaStream_t st);
+int launch_split_merge(Ctx& c, void* out, float* lse, float v_scale, int max_rows_per_head, bool extend_path,
+                       cudaStream_t st);
 // decode-path tile shape of a configuration: warps of 16 rows per unit (0 if
 // max_qo_len * group exceeds 128) and K/V pages per pipeline stage
 int decode_row_warps(const pkv_config& cfg);
