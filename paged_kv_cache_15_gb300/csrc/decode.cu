@@ -66,7 +66,10 @@ struct DecodeCfg {
   static constexpr int STAGES = STAGES_;
   static constexpr int kConsumerWarps = WR * WK;
   static constexpr int kThreads = (kConsumerWarps + 1) * 32;
-  static constexpr int kMinBlocks = kThreads <= 160 ? 2 : 1;  // two CTAs per SM hide latency for the decode shapes
+  // two CTAs per SM hide latency for the decode shapes; 4-bit pools, whose
+  // stages are small and whose widening is bound by instructions, take three
+  // while one row tile leaves the registers for it
+  static constexpr int kMinBlocks = FP4 && RT_ == 1 ? 3 : kThreads <= 160 ? 2 : 1;
   static constexpr int kRows = 8 * RT;
   static constexpr int kStageKeys = WK * KPW;
   static constexpr int kStagePages = kStageKeys / kSegSlots;
@@ -90,7 +93,7 @@ struct DecodeCfg {
   static constexpr int kUnitQOffset = kAbortOffset + 16;  // unit queue: 2 full + 2 empty barriers, 2 ids
   static constexpr int kSmemBytes = kUnitQOffset + 40 + 1024;  // + alignment slack
   static_assert(FP4 || (kRowBytesK % 128 == 0 && kRowBytesV % 128 == 0), "rows must be whole 128-byte swizzle spans");
-  static_assert(!FP4 || (DK == 128 && DV == 128 && kStagePages <= 16 && KPW == 32), "4-bit tiles of 128-wide heads, one lane a copy");
+  static_assert(!FP4 || (DK == 128 && DV == 128 && kStagePages == 8 && KPW == 32), "4-bit tiles of 128-wide heads, one lane a copy");
   static_assert(KPW % 16 == 0 && kStageKeys % kSegSlots == 0, "stage must hold whole pages");
   static_assert(kOwnScratch || WK * 16 * DV * 4 <= kStageBytes, "merge scratch must fit in one stage");
   static_assert(WK > 1 && RT >= 1 && RT <= 2, "key-major tiles: one or two 8-row tiles, key warps combined");
@@ -107,7 +110,6 @@ struct DecodeArgs {
   const uint64_t* tree;  // draft-tree mask word per query token, or null (chain drafts)
   const float* sinks;    // sink logit per query head, or null
   ScoreMods mods;        // score cap and distance bias (kExtrasScores)
-  const uint8_t *k_pool, *v_pool;  // the pools' bytes (4-bit pools: bulk copies of their tiles)
 };
 
 // 4-bit tiles: MMA key row i of a 16-key block holds key fp4_key(i) of the
@@ -115,24 +117,28 @@ struct DecodeArgs {
 // different halves of the banks.
 __device__ __forceinline__ int fp4_key(int i) { return i ^ ((i >> 1) & 1); }
 
-__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr, int at) {
+  addr += at;
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
+__device__ __forceinline__ uint2 lds_v2(uint32_t addr, int at) {
+  addr += at;
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+__device__ __forceinline__ uint16_t lds_u16(uint32_t addr, int at) {
+  addr += at;
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr));
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr, int at) {
+  addr += at;
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 
@@ -305,13 +311,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
   if (C::FP4 && warp == C::kConsumerWarps) {
     // ------------------------------------------------------------ producer of 4-bit tiles
     // The units and their queue are those of the producer below. Each 16-slot
-    // tile of a head is one contiguous run: lane p copies the stage's p-th K
-    // tile, lane 16 + p its p-th V tile, and the next stage's segment indices
-    // are on their way meanwhile.
+    // tile of a head is one row of the pool's map (1,152 bytes), and a gather
+    // brings four of them; rows past the unit's last segment point outside the
+    // map and are filled with zeros without a read. Lane p holds the stage's
+    // p-th segment index; the next stage's are on their way meanwhile.
     const uint64_t pol = policy_evict_first();
-    const int p = lane & 15;
-    const bool is_v = lane >= 16;
-    const uint8_t* const pool = is_v ? a.v_pool : a.k_pool;
+    const int p = lane & 7;
+    if (elect_one()) {
+      prefetch_tmap(&tmap_k);
+      prefetch_tmap(&tmap_v);
+    }
     int slot = 0;
     uint32_t phase = 0;
     uint32_t armed = 0, armed_phase = 0;
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
     const bool hold_first = blockIdx.x == 0 && __ldcg(plan + kHoldLoad) != 0;
     for (int iu = 0; !stop; ++iu) {
       const int q = iu & 1;
-      if (!mbar_wait_warp(&uq_empty[q], ((iu >> 1) & 1) ^ 1, plan, s_abort)) {
+      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&uq_empty[q], ((iu >> 1) & 1) ^ 1, plan, s_abort))) {
         *s_abort = 1;
         break;
       }
@@ -338,21 +347,27 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
       const int nst = (npages + C::kStagePages - 1) / C::kStagePages;
       int next = p < min(C::kStagePages, npages) ? a.m.seg_indices[base + p] : 0;
       for (int st = 0; st < nst; ++st) {
-        const int page = next;
         const int np = min(C::kStagePages, npages - st * C::kStagePages);
+        const int row = p < np ? next * a.num_kv_heads + g : 0x7fffffff;
         const int left = npages - (st + 1) * C::kStagePages;
         next = p < min(C::kStagePages, left) ? a.m.seg_indices[base + (st + 1) * C::kStagePages + p] : 0;
-        if (!mbar_wait_warp(&empty[slot], phase ^ 1, plan, s_abort)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_sleep(&empty[slot], phase ^ 1, plan, s_abort))) {
           *s_abort = 1;
           stop = true;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(np * (fp4_tile_bytes(DK) + fp4_tile_bytes(DV))));
-        __syncwarp();
-        if (p < np && !(hold_first && iu == 0 && st == 0)) {
-          constexpr int kBytes = fp4_tile_bytes(DK);  // (DV == DK)
-          uint8_t* dst = smem + slot * C::kStageBytes + (is_v ? C::kTileBytesK : 0) + p * kBytes;
-          bulk_load_hint(dst, pool + ((long long)page * a.num_kv_heads + g) * kBytes, kBytes, &full[slot], pol);
+        constexpr int kBytes = fp4_tile_bytes(DK);  // (DV == DK)
+        const bool leader = elect_one();
+        if (leader) mbar_arrive_expect_tx(&full[slot], (uint32_t)C::kStageBytes);
+#pragma unroll
+        for (int i = 0; i < C::kStagePages / 4; ++i) {
+          const int y0 = __shfl_sync(0xffffffffu, row, 4 * i), y1 = __shfl_sync(0xffffffffu, row, 4 * i + 1);
+          const int y2 = __shfl_sync(0xffffffffu, row, 4 * i + 2), y3 = __shfl_sync(0xffffffffu, row, 4 * i + 3);
+          if (leader && !(hold_first && iu == 0 && st == 0)) {
+            uint8_t* dst = smem + slot * C::kStageBytes + 4 * i * kBytes;
+            tma_gather4_hint(dst, &tmap_k, 0, y0, y1, y2, y3, &full[slot], pol);
+            tma_gather4_hint(dst + C::kTileBytesK, &tmap_v, 0, y0, y1, y2, y3, &full[slot], pol);
+          }
         }
         armed |= 1u << slot;
         armed_phase = (armed_phase & ~(1u << slot)) | (phase << slot);
@@ -551,6 +566,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
       auto kcol = [&](int mt, int hi) { return C::FP8 ? 16 * mt + 2 * g8 + hi : 16 * mt + 8 * hi + g8; };
       // key of the 16-key block that this lane's MMA row g8 holds (row g8 + 8: that + 8)
       const int krow = C::FP4 ? fp4_key(g8) : g8;
+      // 4-bit tiles: this lane's offsets in a K tile (codes, scales of MMA row
+      // g8; row g8 + 8: half a tile on) and in a V tile (keys of its MMA pair).
+      // Opaque to the compiler, which otherwise computes them anew every step.
+      uint32_t k_codes = krow * (DK / 2) + 16 * t4, k_scales = kSegSlots * (DK / 2) + krow * (DK / 16) + 2 * t4;
+      uint32_t v_codes[2], v_scales[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = fp4_key(2 * t4 + i);
+        v_codes[i] = key * (DV / 2) + 8 * g8;
+        v_scales[i] = kSegSlots * (DV / 2) + key * (DV / 16) + g8;
+      }
+      if constexpr (C::FP4) {
+        asm volatile("" : "+r"(k_codes), "+r"(k_scales), "+r"(v_codes[0]), "+r"(v_codes[1]));
+        asm volatile("" : "+r"(v_scales[0]), "+r"(v_scales[1]));
+      }
       // distance slopes of this lane's rows, in the log2 domain
       float slope[RT][2];
       if constexpr (EXTRAS == kExtrasScores) {
@@ -606,45 +636,45 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
           constexpr float kSlack = 8.f;
           const int kr0 = wk * C::KPW, abs0 = stage_key0 + kr0;
           if (!skip && abs0 < key_end) {
-            const bool two = abs0 + 16 < key_end;
             const float scale = EXTRAS == kExtrasScores ? 1.f : a.scale_log2;
             // S^T = K Q^T of block kb. Lane: 32 codes (two blocks of columns) of
             // key rows g8 and g8 + 8, times their block scales (exact in f16: at
             // most 6 significant bits)
             float s[2][RT][4];
             auto scores = [&](int kb) {
-              const uint32_t tile = kbase + (kr0 / kSegSlots + kb) * fp4_tile_bytes(DK);
+              const uint32_t tile = kbase + kr0 / kSegSlots * fp4_tile_bytes(DK);
               uint32_t kf[2][16];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int row = krow + 8 * h;
-                const uint4 x = lds_v4(tile + row * (DK / 2) + 16 * t4);
-                const uint32_t sc =
-                    e4m3x2_to_f16x2((uint16_t)lds_u16(tile + kSegSlots * (DK / 2) + row * (DK / 16) + 2 * t4));
-                const uint32_t s0 = __byte_perm(sc, 0, 0x1010), s1 = __byte_perm(sc, 0, 0x3232);
+                const uint4 x = lds_v4(tile + k_codes, kb * fp4_tile_bytes(DK) + 8 * h * (DK / 2));
+                const uint32_t sc = e4m3x2_to_f16x2(lds_u16(tile + k_scales, kb * fp4_tile_bytes(DK) + 8 * h * (DK / 16)));
                 e2m1x8_to_f16x2(x.x, kf[h]);
                 e2m1x8_to_f16x2(x.y, kf[h] + 4);
                 e2m1x8_to_f16x2(x.z, kf[h] + 8);
                 e2m1x8_to_f16x2(x.w, kf[h] + 12);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) kf[h][i] = mul_f16x2(kf[h][i], i < 8 ? s0 : s1);
+                for (int i = 0; i < 16; ++i) kf[h][i] = i < 8 ? mul_f16x2_by<false>(kf[h][i], sc) : mul_f16x2_by<true>(kf[h][i], sc);
               }
+              // two chains of MMAs, even and odd k-steps
+              float odd[RT][4];
 #pragma unroll
-              for (int j = 0; j < RT; ++j) s[kb][j][0] = s[kb][j][1] = s[kb][j][2] = s[kb][j][3] = 0.f;
+              for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[kb][j][i] = odd[j][i] = 0.f;
 #pragma unroll
               for (int kk = 0; kk < DK / 16; ++kk) {
                 const uint32_t ka[4] = {kf[0][2 * kk], kf[1][2 * kk], kf[0][2 * kk + 1], kf[1][2 * kk + 1]};
 #pragma unroll
-                for (int j = 0; j < RT; ++j) mma_f16(s[kb][j], ka, qf[kk][j][0], qf[kk][j][1]);
+                for (int j = 0; j < RT; ++j) mma_f16(kk & 1 ? odd[j] : s[kb][j], ka, qf[kk][j][0], qf[kk][j][1]);
               }
-            };
-            scores(0);
-            if (two) {
-              scores(1);
-            } else {
 #pragma unroll
-              for (int j = 0; j < RT; ++j) s[1][j][0] = s[1][j][1] = s[1][j][2] = s[1][j][3] = -INFINITY;
-            }
+              for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[kb][j][i] += odd[j][i];
+            };
+            // (a block past the last segment holds zeros: masked, and no value)
+            scores(0);
+            scores(1);
             // score changes and masks; steps that every row sees whole skip them
             const bool whole = EXTRAS != kExtrasScores && abs0 + 31 < key_end && abs0 + 31 <= prefix &&
                                !(tree && abs0 + 31 >= prefix);
@@ -726,20 +756,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
             // 2mt, m-row g8 + 8 the next. Two keys' codes of a column are brought
             // together in one byte, so a conversion gives the A register's key pair.
             auto values = [&](int kb) {
-              const uint32_t tile = vbase + (kr0 / kSegSlots + kb) * fp4_tile_bytes(DV);
+              const uint32_t tile = vbase + kr0 / kSegSlots * fp4_tile_bytes(DV);
               uint32_t vf[2][2][8];  // [key half][column parity][mt]
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int k0 = fp4_key(2 * t4) + 8 * h, k1 = fp4_key(2 * t4 + 1) + 8 * h;
-                const uint2 x = lds_v2(tile + k0 * (DV / 2) + 8 * g8), y = lds_v2(tile + k1 * (DV / 2) + 8 * g8);
-                const uint32_t scales = tile + kSegSlots * (DV / 2) + g8;
+                const int at = kb * fp4_tile_bytes(DV) + 8 * h * (DV / 2);
+                const int scale_at = kb * fp4_tile_bytes(DV) + 8 * h * (DV / 16);
+                const uint2 x = lds_v2(tile + v_codes[0], at), y = lds_v2(tile + v_codes[1], at);
                 const uint32_t sc = e4m3x2_to_f16x2(
-                    (uint16_t)(lds_u8(scales + k0 * (DV / 16)) | (lds_u8(scales + k1 * (DV / 16)) << 8)));
-                constexpr uint32_t kLow = 0x0f0f0f0fu;
-                e2m1x8_to_f16x2((x.x & kLow) | ((y.x << 4) & ~kLow), vf[h][0]);
-                e2m1x8_to_f16x2((x.y & kLow) | ((y.y << 4) & ~kLow), vf[h][0] + 4);
-                e2m1x8_to_f16x2(((x.x >> 4) & kLow) | (y.x & ~kLow), vf[h][1]);
-                e2m1x8_to_f16x2(((x.y >> 4) & kLow) | (y.y & ~kLow), vf[h][1] + 4);
+                    (uint16_t)__byte_perm(lds_u8(tile + v_scales[0], scale_at), lds_u8(tile + v_scales[1], scale_at), 0x0040));
+                e2m1x8_to_f16x2(low_high_nibbles(x.x, y.x << 4), vf[h][0]);
+                e2m1x8_to_f16x2(low_high_nibbles(x.y, y.y << 4), vf[h][0] + 4);
+                e2m1x8_to_f16x2(low_high_nibbles(x.x >> 4, y.x), vf[h][1]);
+                e2m1x8_to_f16x2(low_high_nibbles(x.y >> 4, y.y), vf[h][1] + 4);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   vf[h][0][i] = mul_f16x2(vf[h][0][i], sc);
@@ -754,7 +783,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
               }
             };
             values(0);
-            if (two) values(1);
+            values(1);
           }
         } else if (!skip) {
 #pragma unroll
@@ -1130,13 +1159,22 @@ int run_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   const uint32_t box_inner = 128 / C::kElem;
   // L2 fills no wider than one head's row of an E4M3 pool (128 bytes)
   const CUtensorMapL2promotion promo = C::FP8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-  // (4-bit tiles come by untiled bulk copies)
-  if (!C::FP4 && encode_tmap_2d(&tk, dt, const_cast<void*>(k_pool), inner_k, slots, inner_k * C::kElem, box_inner,
-                                kSegSlots, CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
+  if (C::FP4) {
+    // one row a tile, as 8-byte words (a box holds at most 256 elements)
+    const uint64_t rows = slots / kSegSlots * (uint64_t)c.cfg.num_kv_heads;
+    const uint32_t words = fp4_tile_bytes(C::DK) / 8;
+    if (rows >= 0x7fffffffull) return PKV_ERR_UNSUPPORTED;
+    if (encode_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, const_cast<void*>(k_pool), words, rows, words * 8, words, 1,
+                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) != PKV_OK ||
+        encode_tmap_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, const_cast<void*>(v_pool), words, rows, words * 8, words, 1,
+                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) != PKV_OK)
+      return PKV_ERR_CUDA;
+  } else if (encode_tmap_2d(&tk, dt, const_cast<void*>(k_pool), inner_k, slots, inner_k * C::kElem, box_inner,
+                            kSegSlots, CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK ||
+             encode_tmap_2d(&tv, dt, const_cast<void*>(v_pool), inner_v, slots, inner_v * C::kElem, box_inner,
+                            kSegSlots, CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK) {
     return PKV_ERR_CUDA;
-  if (!C::FP4 && encode_tmap_2d(&tv, dt, const_cast<void*>(v_pool), inner_v, slots, inner_v * C::kElem, box_inner, kSegSlots,
-                     CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
-    return PKV_ERR_CUDA;
+  }
   DecodeArgs a;
   a.m = make_meta(c);
   a.q = static_cast<const uint16_t*>(q);
@@ -1151,8 +1189,6 @@ int run_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   a.tree = active_tree(c);
   a.sinks = c.sinks;
   a.mods = score_mods(c, a.scale_log2);
-  a.k_pool = static_cast<const uint8_t*>(k_pool);
-  a.v_pool = static_cast<const uint8_t*>(v_pool);
   const int extras = extras_of(c);
   auto kernel = extras == kExtrasScores ? decode_splitkv_kernel<C, kExtrasScores>
                 : extras == kExtrasMask ? decode_splitkv_kernel<C, kExtrasMask>
@@ -1175,7 +1211,7 @@ using DecFp8D128_1 = DecodeCfg<128, 128, PKV_KV_FP8_E4M3, 4, 32, 3, 1>;
 using DecFp8D128_2 = DecodeCfg<128, 128, PKV_KV_FP8_E4M3, 4, 32, 3, 2>;
 using DecBf16D192_1 = DecodeCfg<192, 128, PKV_KV_BF16, 4, 16, 2, 1>;
 using DecBf16D192_2 = DecodeCfg<192, 128, PKV_KV_BF16, 4, 16, 2, 2>;
-using DecFp4D128_1 = DecodeCfg<128, 128, PKV_KV_FP4_E2M1, 4, 32, 4, 1>;
+using DecFp4D128_1 = DecodeCfg<128, 128, PKV_KV_FP4_E2M1, 4, 32, 3, 1>;
 using DecFp4D128_2 = DecodeCfg<128, 128, PKV_KV_FP4_E2M1, 4, 32, 4, 2>;
 
 
@@ -1198,6 +1234,10 @@ int decode_row_warps(const pkv_config& cfg) {
 int decode_stage_pages(const pkv_config& cfg) {
   if (decode_row_warps(cfg) > 1) return kExtendKeys / kSegSlots;
   return cfg.kv_dtype != PKV_KV_BF16 ? 8 : 4;
+}
+
+int decode_ctas_per_sm(const pkv_config& cfg) {
+  return cfg.kv_dtype == PKV_KV_FP4_E2M1 && cfg.max_qo_len * (cfg.num_q_heads / cfg.num_kv_heads) <= 8 ? 3 : 2;
 }
 
 int launch_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, float sm_scale, float k_scale,
@@ -1248,7 +1288,6 @@ int launch_split_merge(Ctx& c, void* out, float* lse, float v_scale, int max_row
   a.tree = nullptr;
   a.sinks = c.sinks;
   a.mods = ScoreMods{};  // the merge combines finished partial rows
-  a.k_pool = a.v_pool = nullptr;
   // one warp per (token, head) row, 8 warps per CTA, 3 CTAs per SM
   const long long rows = (long long)c.cfg.max_q_tokens * c.cfg.num_q_heads;
   const long long grid = std::min<long long>((rows + 7) / 8, (long long)c.num_sms * 3);

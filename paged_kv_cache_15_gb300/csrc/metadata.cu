@@ -86,7 +86,7 @@ struct MetaArgs {
   int dec_tc;
   int units_target;      // decode work units to aim for
   int dec_ctas;          // CTAs of the persistent decode grid
-  int fp8;               // E4M3 pools
+  int fp8;               // E4M3 or 4-bit pools
   int ext_grid;          // CTAs of the extend kernel (units are dealt to them by a fixed stride)
   int partial_cap;
   int max_pages_total;
@@ -638,9 +638,9 @@ int launch_build_metadata(Ctx& c, int batch, const int32_t* seq_lens, const int3
   a.num_kv_heads = c.cfg.num_kv_heads;
   a.stage_pages = decode_stage_pages(c.cfg);
   a.dec_tc = decode_row_warps(c.cfg) > 1 ? 1 : 0;
-  a.units_target = c.decode_ctas * (decode_row_warps(c.cfg) == 1 ? kDecodeTargetWaves : kVerifyTargetWaves);
+  a.units_target = c.decode_ctas * decode_target_waves(c.cfg);
   a.dec_ctas = c.decode_ctas;
-  a.fp8 = c.cfg.kv_dtype == PKV_KV_FP8_E4M3 ? 1 : 0;
+  a.fp8 = c.cfg.kv_dtype != PKV_KV_BF16 ? 1 : 0;
   a.ext_grid = c.extend_ctas;
   a.partial_cap = c.lay.partial_rows_cap;
   a.max_pages_total = c.cfg.max_pages_total;

@@ -69,7 +69,8 @@ void grid_sizes(const pkv_config& cfg, int num_sms, int* decode_ctas, int* exten
       dec_units;  // KV splits of requests whose rows fit one unit
   // two per SM: the decode shapes fit twice; the verify shapes fit once, and
   // the second wave then picks up units as CTAs of the first one finish
-  *decode_ctas = (int)(dec_units < num_sms * 2ll ? dec_units : num_sms * 2ll);
+  const long long dec_slots = (long long)num_sms * decode_ctas_per_sm(cfg);
+  *decode_ctas = (int)(dec_units < dec_slots ? dec_units : dec_slots);
   *extend_ctas = (int)(ext_units < num_sms ? ext_units : num_sms);
   if (*decode_ctas < 1) *decode_ctas = 1;
   if (*extend_ctas < 1) *extend_ctas = 1;

@@ -32,6 +32,7 @@ constexpr int kPageSizeLarge = 128;
 // 128 rows each and pay more per unit
 constexpr int kDecodeTargetWaves = 8;
 constexpr int kVerifyTargetWaves = 4;
+constexpr int kDecodeTargetWavesFp4 = 4;
 // decode splits of one request at most: the merge reads two per lane (so at
 // most 64); a lone long request then still spreads over the whole grid
 constexpr int kMaxSplitsPerRequest = 64;
@@ -226,6 +227,12 @@ int launch_split_merge(Ctx& c, void* out, float* lse, float v_scale, int max_row
 // max_qo_len * group exceeds 128) and K/V pages per pipeline stage
 int decode_row_warps(const pkv_config& cfg);
 int decode_stage_pages(const pkv_config& cfg);
+inline int decode_target_waves(const pkv_config& cfg) {
+  if (decode_row_warps(cfg) != 1) return kVerifyTargetWaves;
+  return cfg.kv_dtype == PKV_KV_FP4_E2M1 ? kDecodeTargetWavesFp4 : kDecodeTargetWaves;
+}
+// CTAs of the persistent decode grid on one SM
+int decode_ctas_per_sm(const pkv_config& cfg);
 
 // Tensor-map encoding through the driver entry point (no link-time libcuda dependency).
 // promo: the L2 fill granularity of a copy. Pool rows of one head are 256
@@ -308,6 +315,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same, letting the thread sleep for up to hint_ns before it answers false.
+__device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+
 // The wait bound of the context (read once a wait has not succeeded at once).
 __device__ __forceinline__ unsigned long long wait_limit_ns(const int* plan) {
   const unsigned v = (unsigned)__ldcg(plan + kWaitLimitNs);
@@ -345,6 +363,22 @@ __device__ __forceinline__ bool mbar_wait_ab(uint64_t* bar, uint32_t parity, int
   }
 }
 
+// The same bounded wait for warps whose polling would take issue slots from
+// the warps that compute: each try sleeps for up to 10 us.
+__device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, int* plan, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns(), limit = wait_limit_ns(plan);
+  while (true) {
+    for (int i = 0; i < 4; ++i)
+      if (mbar_try_wait_hint(bar, parity, 10000)) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > limit) {
+      record_error(plan, kDevTimeout, 0);
+      return false;
+    }
+  }
+}
+
 // The same wait for a whole warp: every lane waits, and the warp gets one
 // answer (false if any lane gave up).
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int* plan, volatile int* abort_flag) {
@@ -371,6 +405,16 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
       "%3}], [%4], %5;" ::"r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// TMA: rows y0 .. y3 of a 2-D map whose box is one row, each from column x.
+__device__ __forceinline__ void tma_gather4_hint(void* dst, const CUtensorMap* map, int x, int y0, int y1, int y2,
+                                                 int y3, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
 
@@ -468,6 +512,29 @@ __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t v, uint32_t* r) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Both halves of a times the low (HI: high) half of b; the half is picked by
+// the multiply itself.
+template <bool HI>
+__device__ __forceinline__ uint32_t mul_f16x2_by(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (HI)
+    asm("{\n .reg .b16 l, h;\n .reg .b32 s;\n mov.b32 {l, h}, %2;\n mov.b32 s, {h, h};\n mul.rn.f16x2 %0, %1, s;\n}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  else
+    asm("{\n .reg .b16 l, h;\n .reg .b32 s;\n mov.b32 {l, h}, %2;\n mov.b32 s, {l, l};\n mul.rn.f16x2 %0, %1, s;\n}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  return r;
+}
+
+// Nibble by nibble: the low ones of a, the high ones of b.
+__device__ __forceinline__ uint32_t low_high_nibbles(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, 0x0f0f0f0f, 0xd8;" : "=r"(r) : "r"(b), "r"(a));
   return r;
 }
 
