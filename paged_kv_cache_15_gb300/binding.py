@@ -60,6 +60,8 @@ _lib = None
 def lib():
     """Load the CUDA library; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -121,7 +123,7 @@ def _ptr(t: Optional[torch.Tensor]):
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _rows(t: Optional[torch.Tensor], what: str):
@@ -133,10 +135,10 @@ def _rows(t: Optional[torch.Tensor], what: str):
         raise ValueError("expected a CUDA tensor")
     if t.dim() != 3 or t.dtype != torch.bfloat16:
         raise ValueError(f"{what}: expected bf16 [tokens, heads, width]")
-    if t.shape[0] and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+    (n, heads, width), (token, head, column) = t.shape, t.stride()
+    if n and (column != 1 or (heads > 1 and head != width)):
         raise ValueError(f"{what}: expected each token's heads and columns to be contiguous")
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), token if n > 1 else heads * width
 
 
 def _int32(t: torch.Tensor, what: str):
@@ -145,9 +147,16 @@ def _int32(t: torch.Tensor, what: str):
     return _ptr(t)
 
 
+# the current stream's handle without the Stream object around it (0.2 us a call instead of 3)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def pkv_status_string(status: int) -> str:
@@ -215,26 +224,24 @@ def pkv_rope_set_kv_buffer(ctx, k_pool, v_pool, loc, positions, cos_sin, q, k, v
     position's angles and then their sines; q_out: contiguous (q and q_out None: k and v alone)."""
     if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
         raise ValueError("cos_sin: expected fp32 [max_positions, rotary_dim]")
-    n = int(loc.shape[0])
-    if positions.shape[0] != n or any(t is not None and t.shape[0] != n for t in (q, k, v, q_out)):
-        raise ValueError("loc, positions, q, k, v and q_out hold different numbers of tokens")
-    if (q is None) != (q_out is None) or (q is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype)):
-        raise ValueError("q_out: expected a tensor like q")
-    rope = pkv_rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(rotary_offset), int(bool(interleaved)))
-    _ptr(cos_sin)
+    n = len(loc)
+    if len(positions) != n or len(k) != n or len(v) != n:
+        raise ValueError("loc, positions, k and v hold different numbers of tokens")
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or q_out.shape != q.shape or q_out.dtype != q.dtype or len(q) != n:
+            raise ValueError("q_out: expected a tensor like q, and q loc's number of tokens")
+    rope = pkv_rope(_ptr(cos_sin), *cos_sin.shape, rotary_offset, 1 if interleaved else 0)
     (qp, qs), (kp, ks), (vp_, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    _check(lib().pkv_rope_set_kv_buffer(ctx, ctypes.byref(rope), _ptr(k_pool), _ptr(v_pool), _int32(loc, "loc"),
+    _check(lib().pkv_rope_set_kv_buffer(ctx, rope, _ptr(k_pool), _ptr(v_pool), _int32(loc, "loc"),
                                         _int32(positions, "positions"), qp, qs, kp, ks, vp_, vs, _ptr(q_out), n,
-                                        float(k_inv_scale), float(v_inv_scale), _stream(stream)),
-           "pkv_rope_set_kv_buffer")
+                                        k_inv_scale, v_inv_scale, _stream(stream)), "pkv_rope_set_kv_buffer")
 
 
 def pkv_get_kv_buffer(ctx, k_pool, v_pool, loc, k, v, k_scale=1.0, v_scale=1.0, stream=None) -> None:
     """Rows of the pools at slots loc, as bf16, into k and v ([tokens, num_kv_heads, width], contiguous)."""
-    n = int(loc.shape[0])
-    for t in (k, v):
-        if t.dtype != torch.bfloat16 or t.shape[0] != n:
-            raise ValueError("k and v: expected bf16 with loc's number of tokens")
+    n = len(loc)
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or len(k) != n or len(v) != n:
+        raise ValueError("k and v: expected bf16 with loc's number of tokens")
     _check(lib().pkv_get_kv_buffer(ctx, _ptr(k_pool), _ptr(v_pool), _int32(loc, "loc"), _ptr(k), _ptr(v), n,
                                    float(k_scale), float(v_scale), _stream(stream)), "pkv_get_kv_buffer")
 

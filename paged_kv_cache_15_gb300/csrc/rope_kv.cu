@@ -80,6 +80,14 @@ __device__ __forceinline__ uint2 quant_fp4(const float* y, uint8_t* scale) {
   return make_uint2(w[0], w[1]);
 }
 
+// 16 bytes of an input row; volatile, so that it stays ahead of the loads whose
+// chain it is to overlap.
+__device__ __forceinline__ uint4 load_row(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 struct RopeKvArgs {
   const uint16_t *q, *k, *v;  // bf16 rows, token i at i * stride elements
   long long q_stride, k_stride, v_stride;
@@ -141,73 +149,85 @@ __global__ void __launch_bounds__(kThreads) rope_kv_kernel(RopeKvArgs a) {
   const int cb = (int)(t - unit * CB);
   const long long tok = unit / per_token;
   int u = (int)(unit - tok * per_token);
+  const bool is_q = u < a.q_units;
+  const bool is_v = u >= a.q_units + a.kv_units;
+  if (!is_q) u -= is_v ? a.q_units + a.kv_units : a.q_units;
+  const int heads = is_q ? a.num_q_heads : a.num_kv_heads;
+  const int h0 = u * RPT, h1 = min(heads, h0 + RPT);
+  if (is_v && cb * 16 >= DV) return;
+  // The rows are requested first, the token's position and slot after them:
+  // the chain position -> angles then runs while the rows are on their way.
+  const int width = is_v ? DV : DK;
+  const uint16_t* src = (is_q   ? a.q + tok * a.q_stride
+                         : is_v ? a.v + tok * a.v_stride
+                                : a.k + tok * a.k_stride);
+  // rotation of the two 8-column vectors of this thread: whether, partner
+  // column, first angle, sign of the sin term
+  const int half = a.rotary / 2;
+  int partner[2], angle[2];
+  bool rot[2], low[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const int col = cb * 16 + 8 * v, rel = col - a.first;
+    rot[v] = ROT != kRotNone && !is_v && rel >= 0 && rel < a.rotary;
+    low[v] = rel < half;
+    partner[v] = ROT == kRotHalf && rot[v] ? (low[v] ? col + half : col - half) : col;
+    angle[v] = ROT == kRotHalf ? (low[v] ? rel : rel - half) : rel / 2;
+  }
+  uint4 own[RPT][2], other[RPT][2];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const uint16_t* row = src + min(h0 + i, h1 - 1) * width;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      own[i][v] = load_row(row + cb * 16 + 8 * v);
+      if (ROT == kRotHalf) other[i][v] = load_row(row + partner[v]);
+    }
+  }
   const int pos = ROT != kRotNone ? a.pos[tok] : 0;
   const long long slot = a.loc[tok];
   if (ROT != kRotNone && (pos < 0 || pos >= a.max_pos)) {
-    if (cb == 0 && u == 0) record_error(a.plan, PKV_DEV_BAD_POSITION, (int)tok);
+    if (cb == 0 && unit == tok * per_token) record_error(a.plan, PKV_DEV_BAD_POSITION, (int)tok);
     return;
   }
-  const bool is_q = u < a.q_units;
-  const bool is_v = u >= a.q_units + a.kv_units;
-  if (!is_q) {
-    u -= is_v ? a.q_units + a.kv_units : a.q_units;
-    if (slot < 0 || slot >= a.num_slots) {
-      if (cb == 0 && u == 0 && !is_v) record_error(a.plan, PKV_DEV_BAD_SLOT, (int)tok);
-      return;
-    }
+  if (!is_q && (slot < 0 || slot >= a.num_slots)) {
+    if (cb == 0 && u == 0 && !is_v) record_error(a.plan, PKV_DEV_BAD_SLOT, (int)tok);
+    return;
   }
-  const int heads = is_q ? a.num_q_heads : a.num_kv_heads;
-  const int h0 = u * RPT, h1 = min(heads, h0 + RPT);
   if (is_v) {
-    if (cb * 16 >= DV) return;
-    const uint16_t* src = a.v + tok * a.v_stride + cb * 16;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int h = h0 + i;
       if (h >= h1) break;
-      const uint4* p = reinterpret_cast<const uint4*>(src + h * DV);
-      const uint4 x0 = __ldcs(p), x1 = __ldcs(p + 1);
       if constexpr (KV == PKV_KV_BF16) {
-        store_bf16<DV>(a.v_pool, slot, heads, h, cb, x0, x1);
+        store_bf16<DV>(a.v_pool, slot, heads, h, cb, own[i][0], own[i][1]);
       } else {
         float x[16];
-        widen8(x0, x);
-        widen8(x1, x + 8);
+        widen8(own[i][0], x);
+        widen8(own[i][1], x + 8);
         store_coded<DV, KV>(a.v_pool, slot, heads, h, cb, x, a.v_inv);
       }
     }
     return;
   }
-  // the two 8-column vectors of this thread: rotated or not, partner column,
-  // sign of the sin term, and their cos and sin
-  const int half = a.rotary / 2;
   float c[16], s[16];
-  int partner[2];
-  bool rot[2];
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
-    const int col = cb * 16 + 8 * v, rel = col - a.first;
-    rot[v] = ROT != kRotNone && rel >= 0 && rel < a.rotary;
-    partner[v] = col;
     if (!rot[v]) continue;
-    const float* row = a.cos_sin + (long long)pos * a.rotary;
+    const float* row = a.cos_sin + (long long)pos * a.rotary + angle[v];
     if constexpr (ROT == kRotHalf) {
-      const bool low = rel < half;
-      const int j = low ? rel : rel - half;
-      partner[v] = low ? col + half : col - half;
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
-        const float4 cc = *reinterpret_cast<const float4*>(row + j + i);
-        const float4 ss = *reinterpret_cast<const float4*>(row + half + j + i);
-        const float sg = low ? -1.f : 1.f;  // (an exact change of sign)
+        const float4 cc = *reinterpret_cast<const float4*>(row + i);
+        const float4 ss = *reinterpret_cast<const float4*>(row + half + i);
+        const float sg = low[v] ? -1.f : 1.f;  // (an exact change of sign)
         c[8 * v + i] = cc.x, c[8 * v + i + 1] = cc.y, c[8 * v + i + 2] = cc.z, c[8 * v + i + 3] = cc.w;
         s[8 * v + i] = sg * ss.x, s[8 * v + i + 1] = sg * ss.y, s[8 * v + i + 2] = sg * ss.z;
         s[8 * v + i + 3] = sg * ss.w;
       }
     } else {
-      const int j = rel / 2;
-      const float4 cc = *reinterpret_cast<const float4*>(row + j);
-      const float4 ss = *reinterpret_cast<const float4*>(row + half + j);
+      const float4 cc = *reinterpret_cast<const float4*>(row);
+      const float4 ss = *reinterpret_cast<const float4*>(row + half);
       const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -217,7 +237,6 @@ __global__ void __launch_bounds__(kThreads) rope_kv_kernel(RopeKvArgs a) {
       }
     }
   }
-  const uint16_t* src = is_q ? a.q + tok * a.q_stride : a.k + tok * a.k_stride;
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int h = h0 + i;
@@ -226,11 +245,11 @@ __global__ void __launch_bounds__(kThreads) rope_kv_kernel(RopeKvArgs a) {
     uint4 out[2];  // as bf16; columns that are not rotated keep their bits
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      out[v] = *reinterpret_cast<const uint4*>(src + h * DK + cb * 16 + 8 * v);
-      widen8(out[v], x + 8 * v);
+      out[v] = own[i][v];
+      widen8(own[i][v], x + 8 * v);
       float p[8];
       if constexpr (ROT == kRotHalf) {
-        widen8(*reinterpret_cast<const uint4*>(src + h * DK + partner[v]), p);
+        widen8(other[i][v], p);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) p[e] = x[8 * v + (e ^ 1)];
