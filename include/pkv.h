@@ -333,8 +333,8 @@ int pkv_set_attention_sinks(pkv_ctx* ctx, const float* d_sinks);
  *   cap * tanh(s_j / cap)
  * before the bias below, the masks, the softmax and the sinks. 0 (the default)
  * turns it off. Applies to every forward of the context until set again; a
- * captured graph keeps the value of its capture. Errors: INVALID_ARG (negative,
- * infinite or NaN). */
+ * captured graph keeps the value of its capture. Errors: INVALID_ARG (neither 0
+ * nor in [1e-30, 1e30]). */
 int pkv_set_logit_cap(pkv_ctx* ctx, float cap);
 
 /* Bias by distance: with slopes set (device fp32 [num_q_heads]), head h's score

@@ -68,6 +68,11 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -130,12 +135,14 @@ __device__ __forceinline__ float max32(const uint32_t* sr, float m) {
 }
 
 // p = exp2(s * scale - ref) for 32 raw scores: packed bf16 (F16: f16) pairs
-// into pk, running sums in four packed accumulators.
-template <bool F16>
+// into pk, running sums in four packed accumulators. READY: sr holds s * scale -
+// ref already.
+template <bool F16, bool READY>
 __device__ __forceinline__ void exp32(const uint32_t* sr, uint64_t sc2, uint64_t nref2, uint32_t* pk, uint64_t* acc) {
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
-    const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, nref2);
+    const uint64_t s2 = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+    const uint64_t x = READY ? s2 : f2_fma(s2, sc2, nref2);
     const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
     acc[(c >> 1) & 3] = f2_add(acc[(c >> 1) & 3], f2_pack(p0, p1));
     pk[c >> 1] = F16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
@@ -997,29 +1004,55 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
           }
           fence_proxy_async_smem();
         }
-        // (scores with a cap or bias leave load_s in the log2 domain)
+        // (scores with a cap or bias leave load_s in the log2 domain, less the reference)
         const float scale = EXTRAS == kExtrasScores ? 1.f : a.scale_log2;
         const uint64_t sc2 = f2_pack(scale, scale);
         uint32_t pk[kExtendKeys / 2];  // P as bf16 pairs, written to TMEM once final
         // S read 64 columns per TMEM wait; masked keys become -inf
-        auto load_s = [&](int cc, uint32_t* sr) {
+        auto load_s = [&](int cc, uint32_t* sr, float nref) {
           tmem_ld32(lane_base + s_col + cc * 32, sr);
           tmem_ld32(lane_base + s_col + cc * 32 + 32, sr + 32);
           tmem_wait_ld();
           if constexpr (EXTRAS == kExtrasScores) {
-            // score cap, then distance bias (one uniform branch for the 64 scores)
-            if (a.mods.cap2 != 0.f) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) sr[i] = __float_as_uint(capped_score(a.mods, __uint_as_float(sr[i])));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) * a.scale_log2);
-            }
+            // score cap, then distance bias, then the reference off: the log2
+            // domain's s - m_ref in one last fused multiply-add
+            float base = nref, step = 0.f;
             if (a.mods.slopes) {
-              const float d0 = (float)(key0 + cc * 32 - limit);
+              step = slope;
+              base = fmaf(slope, (float)(key0 + cc * 32 - limit), nref);
+            }
+            bool near = false;
+            if (a.mods.cap2 != 0.f) {
+              // (keys behind the row's limit may hold anything: masked below)
+              float far = 0.f;
+#pragma unroll
+              for (int i = 0; i < 64; i += 2)
+                far = max3f(far, fabsf(__uint_as_float(sr[i])), fabsf(__uint_as_float(sr[i + 1])));
+              near = __all_sync(0xffffffffu, far <= a.mods.near);
+              if (!near) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                  sr[i] = __float_as_uint(fmaf(step, (float)i, capped_score(a.mods, __uint_as_float(sr[i])) + base));
+              }
+            }
+            if (near) {
+              const uint64_t step2 = f2_pack(step, step), base2 = f2_pack(base, base);
+#pragma unroll
+              for (int i = 0; i < 64; i += 2) {
+                const uint64_t raw = f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+                const uint64_t v = C::FP4 ? f2_mul(raw, f2_pack(a.mods.unit, a.mods.unit)) : raw;
+                const uint64_t u = f2_mul(v, v);
+                uint64_t p = f2_pack(a.mods.q[3], a.mods.q[3]);
+#pragma unroll
+                for (int k = 2; k >= 0; --k) p = f2_fma(p, u, f2_pack(a.mods.q[k], a.mods.q[k]));
+                p = f2_fma(raw, p, a.mods.slopes ? f2_fma(step2, f2_pack((float)i, (float)(i + 1)), base2) : base2);
+                sr[i] = __float_as_uint(f2_lo(p));
+                sr[i + 1] = __float_as_uint(f2_hi(p));
+              }
+            } else if (a.mods.cap2 == 0.f) {
 #pragma unroll
               for (int i = 0; i < 64; ++i)
-                sr[i] = __float_as_uint(fmaf(slope, d0 + (float)i, __uint_as_float(sr[i])));
+                sr[i] = __float_as_uint(fmaf(__uint_as_float(sr[i]), a.scale_log2, fmaf(step, (float)i, base)));
             }
           }
           if (diag) {
@@ -1039,9 +1072,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
 #pragma unroll
           for (int cc = 0; cc < kExtendKeys / 32; cc += 2) {
             uint32_t sr[64];
-            load_s(cc, sr);
-            exp32<C::CODED>(sr, sc2, nref2, pk + cc * 16, acc);
-            exp32<C::CODED>(sr + 32, sc2, nref2, pk + cc * 16 + 16, acc);
+            load_s(cc, sr, -m_ref);
+            exp32<C::CODED, EXTRAS == kExtrasScores>(sr, sc2, nref2, pk + cc * 16, acc);
+            exp32<C::CODED, EXTRAS == kExtrasScores>(sr + 32, sc2, nref2, pk + cc * 16 + 16, acc);
           }
           const uint64_t accs = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
           return f2_lo(accs) + f2_hi(accs);
@@ -1064,7 +1097,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
 #pragma unroll
           for (int cc = 0; cc < kExtendKeys / 32; cc += 2) {
             uint32_t sr[64];
-            load_s(cc, sr);
+            load_s(cc, sr, 0.f);
             mx = max32(sr + 32, max32(sr, mx));
           }
           const float mt = mx * scale;

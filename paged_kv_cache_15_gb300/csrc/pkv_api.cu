@@ -480,7 +480,8 @@ int pkv_set_attention_sinks(pkv_ctx* ctx, const float* d_sinks) {
 }
 
 int pkv_set_logit_cap(pkv_ctx* ctx, float cap) {
-  if (!ctx || !(cap >= 0.f) || !std::isfinite(cap)) return PKV_ERR_INVALID_ARG;
+  // (the bounds keep cap * log2(e) and its quotients inside fp32)
+  if (!ctx || !(cap == 0.f || (cap >= 1e-30f && cap <= 1e30f))) return PKV_ERR_INVALID_ARG;
   ctx->logit_cap = cap;
   return PKV_OK;
 }

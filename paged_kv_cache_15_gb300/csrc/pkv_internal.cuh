@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <utility>
 
 #include "../../include/pkv.h"
@@ -151,18 +152,41 @@ constexpr float kLn2 = 0.6931471805599453f;
 // domain: with t = raw * scale_log2,
 //   cap:   t <- cap2 * tanh(t / cap2) = cap2 - 2 * cap2 / (1 + 2^(raw * cap_k))
 //   bias:  t <- t + slope * log2(e) * (key position - query position)
-// The quotient form loses nothing that matters: its absolute error is about
-// 2^-22 * cap2 (cap2 is cap * log2 e), 2e-5 for a cap of 50.
+// Near zero, where most scores are, tanh(x) / x is a polynomial in x^2 instead
+// (relative error 1e-7 up to |x| = 0.4: a weighted least-squares fit of four
+// coefficients, driven to equal ripples), which leaves the exponential unit to
+// the softmax: t = raw * (q0 + q1 v^2 + ...), v = raw * unit.
 struct ScoreMods {
   float cap2;           // cap * log2(e); 0: no cap
-  float cap_k;          // 2 * scale_log2 / cap2 * log2(e)
+  float cap_k;          // 2 * scale_log2 / cap
+  float near;           // |raw| up to which the polynomial holds
+  float unit;           // 1, or the power of two that brings 4-bit pools' raw scores near 1
+  float q[4];           // the polynomial's coefficients in v^2, scale_log2 included
   const float* slopes;  // per query head, or null
 };
+constexpr float kTanhNear = 0.4f;
 
 inline ScoreMods score_mods(const Ctx& c, float scale_log2) {
   ScoreMods m;
   m.cap2 = c.logit_cap * kLog2e;
   m.cap_k = c.logit_cap > 0.f ? 2.f * scale_log2 / c.logit_cap : 0.f;
+  // x = raw * x_of_raw. Scores of 4-bit pools are in units of the codes, so
+  // large that the last coefficient would underflow: those take one multiply
+  // more (x_of_raw's exponent as the unit).
+  const double x_of_raw = m.cap2 > 0.f ? (double)scale_log2 / m.cap2 : 0.0;
+  int exponent = 0;
+  if (x_of_raw > 0.0 && c.cfg.kv_dtype == PKV_KV_FP4_E2M1) (void)frexp(x_of_raw, &exponent);
+  if (exponent < -100 || exponent > 100) exponent = 0;
+  m.unit = (float)ldexp(1.0, exponent);
+  const double x_of_v = ldexp(x_of_raw, -exponent);
+  const double tanh_coef[4] = {0.9999999019009008, -0.3333136245855499, 0.1327097675244408, -0.047553603353342515};
+  double power = scale_log2;
+  for (int i = 0; i < 4; ++i, power *= x_of_v * x_of_v) m.q[i] = (float)(tanh_coef[i] * power);
+  // A cap far above the scores makes the last coefficients vanish in fp32: the
+  // range shrinks to where their terms are below 1e-7. One far below them makes
+  // them overflow: the quotient, whose error is in units of the cap, serves all.
+  const double reach = m.q[3] < -1e-36f ? kTanhNear : m.q[2] > 1e-36f ? 0.1 : m.q[1] < -1e-36f ? 0.03 : 5e-4;
+  m.near = x_of_raw > 0.0 && m.q[3] > -1e30f ? (float)fmin(reach / x_of_raw, 3e38) : -1.f;
   m.slopes = c.slopes;
   return m;
 }
@@ -562,9 +586,15 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// A raw score, capped, in the log2 domain.
-__device__ __forceinline__ float capped_score(const ScoreMods& m, float raw) {
+// A raw score, capped, in the log2 domain: the quotient, which serves |x| above
+// kTanhNear (its absolute error is about 2^-22 cap2 everywhere).
+__device__ __forceinline__ float capped_far(const ScoreMods& m, float raw) {
   return m.cap2 - 2.f * m.cap2 * fast_rcp(1.f + fast_exp2(raw * m.cap_k));
+}
+__device__ __forceinline__ float capped_score(const ScoreMods& m, float raw) {
+  const float v = raw * m.unit, u = v * v;
+  const float p = fmaf(fmaf(fmaf(m.q[3], u, m.q[2]), u, m.q[1]), u, m.q[0]);
+  return fabsf(raw) <= m.near ? raw * p : capped_far(m, raw);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

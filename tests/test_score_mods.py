@@ -86,6 +86,23 @@ def test_caps_from_flat_to_none(case, cap):
     check(run(W, spec))
 
 
+@pytest.mark.parametrize("case", ["decode_g4", "extend", "verify_tc"])
+@pytest.mark.parametrize("cap", [1e-30, 1e-10, 1e20, 1e30])
+def test_caps_at_the_ends_of_their_range(case, cap):
+    """A vanishing cap leaves every visible key the same weight; a vast one leaves the scores alone, to their last bits."""
+    W, spec = work(case, cap=cap)
+    check(run(W, spec))
+
+
+@pytest.mark.parametrize("case", ["decode_g16", "extend_g3_d64", "verify_prefill"])
+def test_scores_on_both_sides_of_the_polynomial(case):
+    """Scores up to several caps: the polynomial near zero and the quotient beyond it in the same rows."""
+    W, spec = work(case, cap=2.0, gain=1.0)
+    check(run(W, spec))
+    W, spec = work(case, cap=1.7, gain=2.5, slopes=True)
+    check(run(W, spec))
+
+
 @pytest.mark.parametrize("case", ["decode_g4", "extend_long_prefix", "verify_tc"])
 def test_steep_and_positive_and_zero_slopes(case):
     W, spec = work(case, slopes=True)
@@ -156,7 +173,7 @@ def test_off_again_gives_the_plain_results(case):
 def test_refusals():
     W, _ = work("decode_g3_d64")
     d = DeviceBatch(W)
-    for cap in (-1.0, float("nan"), float("inf")):
+    for cap in (-1.0, float("nan"), float("inf"), 1e31, 1e-31):
         with pytest.raises(B.PkvError) as e:
             B.pkv_set_logit_cap(d.ctx, cap)
         assert e.value.status == B.PKV_ERR_INVALID_ARG
