@@ -109,7 +109,7 @@ struct DecodeArgs {
   float v_scale;     // multiplies the output (E4M3 pools), 1 for bf16
   const uint64_t* tree;  // draft-tree mask word per query token, or null (chain drafts)
   const float* sinks;    // sink logit per query head, or null
-  ScoreMods mods;        // score cap and distance bias (kExtrasScores)
+  ScoreMods mods;        // score cap and distance bias (kExtrasBias)
 };
 
 // 4-bit tiles: MMA key row i of a 16-key block holds key fp4_key(i) of the
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
       }
       // distance slopes of this lane's rows, in the log2 domain
       float slope[RT][2];
-      if constexpr (EXTRAS == kExtrasScores) {
+      if constexpr (EXTRAS == kExtrasBias) {
 #pragma unroll
         for (int j = 0; j < RT; ++j)
 #pragma unroll
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
           constexpr float kSlack = 8.f;
           const int kr0 = wk * C::KPW, abs0 = stage_key0 + kr0;
           if (!skip && abs0 < key_end) {
-            const float scale = EXTRAS == kExtrasScores ? 1.f : a.scale_log2;
+            const float scale = EXTRAS == kExtrasBias ? 1.f : a.scale_log2;
             // S^T = K Q^T of block kb. Lane: 32 codes (two blocks of columns) of
             // key rows g8 and g8 + 8, times their block scales (exact in f16: at
             // most 6 significant bits)
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
             scores(0);
             scores(1);
             // score changes and masks; steps that every row sees whole skip them
-            const bool whole = EXTRAS != kExtrasScores && abs0 + 31 < key_end && abs0 + 31 <= prefix &&
+            const bool whole = EXTRAS != kExtrasBias && abs0 + 31 < key_end && abs0 + 31 <= prefix &&
                                !(tree && abs0 + 31 >= prefix);
             if (!whole) {
 #pragma unroll
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
                     for (int h = 0; h < 2; ++h) {
                       const int kp = abs0 + 16 * kb + krow + 8 * h;
                       float& x = s[kb][j][2 * h + e];
-                      if constexpr (EXTRAS == kExtrasScores)
+                      if constexpr (EXTRAS == kExtrasBias)
                         x = (a.mods.cap2 != 0.f ? capped_score(a.mods, x) : x * a.scale_log2) +
                             slope[j][e] * (float)(kp - lim[j][e]);
                       bool ok = kp < key_end && kp <= lim[j][e];
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
               }
             }
             // ---- mask, online softmax over the 16 keys (log2 domain) ----
-            if constexpr (EXTRAS == kExtrasScores) {
+            if constexpr (EXTRAS == kExtrasBias) {
 #pragma unroll
               for (int j = 0; j < RT; ++j)
 #pragma unroll
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) decode_splitkv_ker
               for (int h = 0; h < 2; ++h) {
                 const int kp = abs0 + krow + 8 * h;
                 const bool ok = kp < key_end;
-                const float scale = EXTRAS == kExtrasScores ? 1.f : a.scale_log2;
+                const float scale = EXTRAS == kExtrasBias ? 1.f : a.scale_log2;
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                   s[j][2 * h + e] = (ok && kp <= lim[j][e]) ? s[j][2 * h + e] * scale : -INFINITY;
@@ -1190,7 +1190,7 @@ int run_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   a.sinks = c.sinks;
   a.mods = score_mods(c, a.scale_log2);
   const int extras = extras_of(c);
-  auto kernel = extras == kExtrasScores ? decode_splitkv_kernel<C, kExtrasScores>
+  auto kernel = extras >= kExtrasCap    ? decode_splitkv_kernel<C, kExtrasBias>
                 : extras == kExtrasMask ? decode_splitkv_kernel<C, kExtrasMask>
                                         : decode_splitkv_kernel<C, kExtrasNone>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)

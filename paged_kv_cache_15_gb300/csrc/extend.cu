@@ -276,7 +276,7 @@ struct ExtendArgs {
   // 1: the units are the decode plan's (request, split) items, the decode
   // path's verify shapes (at most 128 rows per KV head); 0: the extend plan
   int dplan;
-  ScoreMods mods;  // score cap and distance bias (kExtrasScores)
+  ScoreMods mods;  // score cap and distance bias (kExtrasCap, kExtrasBias)
   const uint8_t *k_pool, *v_pool;  // the pools' bytes (4-bit pools: bulk copies of their tiles)
 };
 
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
   // inside the batch's tokens (never past the end of the caller's q buffer);
   // otherwise the softmax warps write it.
   // distance bias: KV tiles from the nearest to the farthest
-  const bool rev = EXTRAS == kExtrasScores && a.mods.slopes != nullptr;
+  const bool rev = EXTRAS == kExtrasBias;
   auto q_by_tma = [&](const ExtendTile& u, int x) {
     return a.q_tma != 0 && a.m.qo_indptr[u.b] + (u.row0 + x * kExtendRows) / G + a.q_box_tokens <= total_q;
   };
@@ -898,9 +898,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
       uint64_t tword = ~0ull;
       int draft0 = 0x3fffffff;  // first draft key (none without a tree)
       float slope = 0.f;  // distance slope of the row's head, in the log2 domain
-      if constexpr (EXTRAS == kExtrasScores) {
-        if (a.mods.slopes) slope = a.mods.slopes[g * G + R % G] * kLog2e;
-      }
+      if constexpr (EXTRAS == kExtrasBias) slope = a.mods.slopes[g * G + R % G] * kLog2e;
       if constexpr (EXTRAS != kExtrasNone) {
         if (a.tree) {
           tword = valid ? a.tree[q0 + R / G] : ~0ull;
@@ -967,6 +965,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
       // l: the row's running sum of p
       float m_ref = 0.f, l = 0.f;
       bool aborted = false;
+      // the cap's coefficients as register pairs (opaque: the compiler would
+      // fetch them anew at every use)
+      uint64_t cap_q[4] = {0, 0, 0, 0};
+      if constexpr (EXTRAS >= kExtrasCap) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          cap_q[k] = f2_pack(a.mods.q[k], a.mods.q[k]);
+          asm volatile("" : "+l"(cap_q[k]));
+        }
+      }
       for (int jr = 0; jr < nX; ++jr) {
         const int j = ukv.tile(x, jr);              // absolute KV tile
         const uint32_t jj = jt + ukv.pos(x, jr);    // its place in the V ring sequence
@@ -1004,57 +1012,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
           }
           fence_proxy_async_smem();
         }
-        // (scores with a cap or bias leave load_s in the log2 domain, less the reference)
-        const float scale = EXTRAS == kExtrasScores ? 1.f : a.scale_log2;
-        const uint64_t sc2 = f2_pack(scale, scale);
+        constexpr bool kScores = EXTRAS >= kExtrasCap;
+        const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
         uint32_t pk[kExtendKeys / 2];  // P as bf16 pairs, written to TMEM once final
         // S read 64 columns per TMEM wait; masked keys become -inf
-        auto load_s = [&](int cc, uint32_t* sr, float nref) {
+        auto load_s = [&](int cc, uint32_t* sr) {
           tmem_ld32(lane_base + s_col + cc * 32, sr);
           tmem_ld32(lane_base + s_col + cc * 32 + 32, sr + 32);
           tmem_wait_ld();
-          if constexpr (EXTRAS == kExtrasScores) {
-            // score cap, then distance bias, then the reference off: the log2
-            // domain's s - m_ref in one last fused multiply-add
-            float base = nref, step = 0.f;
-            if (a.mods.slopes) {
-              step = slope;
-              base = fmaf(slope, (float)(key0 + cc * 32 - limit), nref);
-            }
-            bool near = false;
-            if (a.mods.cap2 != 0.f) {
-              // (keys behind the row's limit may hold anything: masked below)
-              float far = 0.f;
-#pragma unroll
-              for (int i = 0; i < 64; i += 2)
-                far = max3f(far, fabsf(__uint_as_float(sr[i])), fabsf(__uint_as_float(sr[i + 1])));
-              near = __all_sync(0xffffffffu, far <= a.mods.near);
-              if (!near) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  sr[i] = __float_as_uint(fmaf(step, (float)i, capped_score(a.mods, __uint_as_float(sr[i])) + base));
-              }
-            }
-            if (near) {
-              const uint64_t step2 = f2_pack(step, step), base2 = f2_pack(base, base);
-#pragma unroll
-              for (int i = 0; i < 64; i += 2) {
-                const uint64_t raw = f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-                const uint64_t v = C::FP4 ? f2_mul(raw, f2_pack(a.mods.unit, a.mods.unit)) : raw;
-                const uint64_t u = f2_mul(v, v);
-                uint64_t p = f2_pack(a.mods.q[3], a.mods.q[3]);
-#pragma unroll
-                for (int k = 2; k >= 0; --k) p = f2_fma(p, u, f2_pack(a.mods.q[k], a.mods.q[k]));
-                p = f2_fma(raw, p, a.mods.slopes ? f2_fma(step2, f2_pack((float)i, (float)(i + 1)), base2) : base2);
-                sr[i] = __float_as_uint(f2_lo(p));
-                sr[i + 1] = __float_as_uint(f2_hi(p));
-              }
-            } else if (a.mods.cap2 == 0.f) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i)
-                sr[i] = __float_as_uint(fmaf(__uint_as_float(sr[i]), a.scale_log2, fmaf(step, (float)i, base)));
-            }
-          }
           if (diag) {
             if constexpr (EXTRAS != kExtrasNone) {
               mask32_bits(sr, visible32(key0 + cc * 32, limit, draft0, tword));
@@ -1065,21 +1030,96 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
             }
           }
         };
+        // Scores with a cap or bias: 32 raw ones (keys from key0 + 32 cc) become
+        // their log2-domain values less the reference (nref = -m_ref), masked
+        // keys -inf. The cap is taken by its polynomial, the largest |raw| kept on
+        // the way (keys behind the row's limit, which may hold anything, at worst
+        // cost a second pass); where that leaves the polynomial's range the
+        // tile's pass runs again with exact set, which picks the polynomial or
+        // the quotient key by key. Packed operations with the coefficients in
+        // registers: the pass is straight-line code of some 700 instructions for
+        // two warps a scheduler, and bound by their number.
+        float big = 0.f;
+        auto scores32 = [&](int cc, uint32_t* sr, float nref, bool exact) {
+          const float base = EXTRAS == kExtrasBias ? fmaf(slope, (float)(key0 + cc * 32 - limit), nref) : nref;
+          if (exact) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float r = __uint_as_float(sr[i]);
+              const float t = EXTRAS == kExtrasBias && a.mods.cap2 == 0.f ? r * a.scale_log2 : capped_score(a.mods, r);
+              sr[i] = __float_as_uint(t + (EXTRAS == kExtrasBias ? fmaf(slope, (float)i, base) : base));
+            }
+          } else {
+            // biases of eight keys, eight slopes further each time
+            uint64_t b[4] = {f2_pack(base, base), 0, 0, 0};
+            if constexpr (EXTRAS == kExtrasBias) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                b[k] = f2_pack(fmaf(slope, (float)(2 * k), base), fmaf(slope, (float)(2 * k + 1), base));
+            }
+            const uint64_t eight = f2_pack(8.f * slope, 8.f * slope);
+            auto bias = [&](int i) {
+              if constexpr (EXTRAS != kExtrasBias) return b[0];
+              const uint64_t now = b[(i >> 1) & 3];
+              b[(i >> 1) & 3] = f2_add(now, eight);
+              return now;
+            };
+            if (EXTRAS == kExtrasBias && a.mods.cap2 == 0.f) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const uint64_t t = f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sc2, bias(i));
+                sr[i] = __float_as_uint(f2_lo(t));
+                sr[i + 1] = __float_as_uint(f2_hi(t));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float r0 = __uint_as_float(sr[i]), r1 = __uint_as_float(sr[i + 1]);
+                big = max3f(big, fabsf(r0), fabsf(r1));
+                const uint64_t raw = f2_pack(r0, r1);
+                const uint64_t v = C::FP4 ? f2_mul(raw, f2_pack(a.mods.unit, a.mods.unit)) : raw;
+                const uint64_t u = f2_mul(v, v);
+                const uint64_t p = f2_fma(f2_fma(f2_fma(cap_q[3], u, cap_q[2]), u, cap_q[1]), u, cap_q[0]);
+                const uint64_t t = f2_fma(raw, p, bias(i));
+                sr[i] = __float_as_uint(f2_lo(t));
+                sr[i + 1] = __float_as_uint(f2_hi(t));
+              }
+            }
+          }
+          if (diag) mask32_bits(sr, visible32(key0 + cc * 32, limit, draft0, tword));
+        };
         // P of the tile against the reference; returns the tile's row sum
-        auto exp_pass = [&]() {
+        auto exp_pass = [&](bool exact) {
           const uint64_t nref2 = f2_pack(-m_ref, -m_ref);
           uint64_t acc[4] = {0, 0, 0, 0};
+          if constexpr (kScores) {
+            // 32 columns at a time, the next 32 on their way meanwhile
+            uint32_t sr[2][32];
+            tmem_ld32(lane_base + s_col, sr[0]);
+            tmem_wait_ld32(sr[0]);
 #pragma unroll
-          for (int cc = 0; cc < kExtendKeys / 32; cc += 2) {
-            uint32_t sr[64];
-            load_s(cc, sr, -m_ref);
-            exp32<C::CODED, EXTRAS == kExtrasScores>(sr, sc2, nref2, pk + cc * 16, acc);
-            exp32<C::CODED, EXTRAS == kExtrasScores>(sr + 32, sc2, nref2, pk + cc * 16 + 16, acc);
+            for (int cc = 0; cc < kExtendKeys / 32; ++cc) {
+              if (cc + 1 < kExtendKeys / 32) tmem_ld32(lane_base + s_col + (cc + 1) * 32, sr[(cc + 1) & 1]);
+              scores32(cc, sr[cc & 1], -m_ref, exact);
+              exp32<C::CODED, true>(sr[cc & 1], sc2, nref2, pk + cc * 16, acc);
+              if (cc + 1 < kExtendKeys / 32) tmem_wait_ld32(sr[(cc + 1) & 1]);
+            }
+          } else {
+#pragma unroll
+            for (int cc = 0; cc < kExtendKeys / 32; cc += 2) {
+              uint32_t sr[64];
+              load_s(cc, sr);
+              exp32<C::CODED, false>(sr, sc2, nref2, pk + cc * 16, acc);
+              exp32<C::CODED, false>(sr + 32, sc2, nref2, pk + cc * 16 + 16, acc);
+            }
           }
           const uint64_t accs = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
           return f2_lo(accs) + f2_hi(accs);
         };
-        float tsum = exp_pass();
+        float tsum = exp_pass(false);
+        if constexpr (kScores) {
+          if (__any_sync(0xffffffffu, a.mods.cap2 != 0.f && !(big <= a.mods.near))) tsum = exp_pass(true);
+        }
         // The tile sum bounds every p of the row: while it is at most 2^16 no p
         // can overflow bf16 P or the fp32 O and l, and the reference (which
         // cancels in O / l) stays put, so the common path needs no row max.
@@ -1094,13 +1134,24 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         const bool need = (!(tsum <= kHigh) || (l == 0.f && tsum < kLow)) && limit >= key0;
         if (__any_sync(0xffffffffu, need)) {
           float mx = -INFINITY;
+          if constexpr (kScores) {
+#pragma unroll 1
+            for (int cc = 0; cc < kExtendKeys / 32; ++cc) {
+              uint32_t sr[32];
+              tmem_ld32(lane_base + s_col + cc * 32, sr);
+              tmem_wait_ld32(sr);
+              scores32(cc, sr, 0.f, true);
+              mx = max32(sr, mx);
+            }
+          } else {
 #pragma unroll
-          for (int cc = 0; cc < kExtendKeys / 32; cc += 2) {
-            uint32_t sr[64];
-            load_s(cc, sr, 0.f);
-            mx = max32(sr + 32, max32(sr, mx));
+            for (int cc = 0; cc < kExtendKeys / 32; cc += 2) {
+              uint32_t sr[64];
+              load_s(cc, sr);
+              mx = max32(sr + 32, max32(sr, mx));
+            }
           }
-          const float mt = mx * scale;
+          const float mt = kScores ? mx : mx * a.scale_log2;
           const bool move = need && mt != -INFINITY && (mt > m_ref || l == 0.f);
           // O_X holds every earlier PV: the s_full commit waited on above was
           // issued after PV_X of the previous tile
@@ -1121,7 +1172,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
             l *= alpha;
             m_ref = mt;
           }
-          tsum = exp_pass();
+          tsum = exp_pass(true);
         }
         // P overwrites the first half of this tile's S columns
         tmem_st32(lane_base + s_col, pk);
@@ -1329,7 +1380,8 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
     a.q_box_tokens = (int)box_tok;
   }
   const int extras = extras_of(c);
-  auto kernel = extras == kExtrasScores ? extend_tc_kernel<C, kExtrasScores>
+  auto kernel = extras == kExtrasBias   ? extend_tc_kernel<C, kExtrasBias>
+                : extras == kExtrasCap  ? extend_tc_kernel<C, kExtrasCap>
                 : extras == kExtrasMask ? extend_tc_kernel<C, kExtrasMask>
                                         : extend_tc_kernel<C, kExtrasNone>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)

@@ -124,7 +124,9 @@ inline const uint64_t* active_tree(const Ctx& c) {
 
 // Which instantiation of the attention kernels a forward takes: plain batches
 // run without the code of the features they do not use.
-enum Extras : int { kExtrasNone = 0, kExtrasMask = 1, kExtrasScores = 2 };  // 1: tree or sinks, 2: score changes too
+// None; tree or sinks; a score cap too; a distance bias too (and a cap, if one
+// is set). The decode kernel has one instantiation for the last two, kExtrasBias.
+enum Extras : int { kExtrasNone = 0, kExtrasMask = 1, kExtrasCap = 2, kExtrasBias = 3 };
 
 // How split units hand their normalised output rows to the merge:
 //   bf16: bf16 and E4M3 pools without score changes;
@@ -140,7 +142,7 @@ enum Extras : int { kExtrasNone = 0, kExtrasMask = 1, kExtrasScores = 2 };  // 1
 enum PartKind : int { kPartBf16 = 0, kPartF16 = 1, kPartF32 = 2 };
 __host__ __device__ constexpr int part_kind(int kv_dtype, int extras) {
   return kv_dtype == PKV_KV_FP4_E2M1   ? kPartF16
-         : extras != kExtrasScores     ? kPartBf16
+         : extras < kExtrasCap         ? kPartBf16
          : kv_dtype == PKV_KV_FP8_E4M3 ? kPartF16
                                        : kPartF32;
 }
@@ -193,7 +195,10 @@ inline ScoreMods score_mods(const Ctx& c, float scale_log2) {
 
 // The instantiation a forward of this context takes.
 inline int extras_of(const Ctx& c) {
-  return c.logit_cap > 0.f || c.slopes ? kExtrasScores : active_tree(c) || c.sinks ? kExtrasMask : kExtrasNone;
+  return c.slopes                     ? kExtrasBias
+         : c.logit_cap > 0.f          ? kExtrasCap
+         : active_tree(c) || c.sinks  ? kExtrasMask
+                                      : kExtrasNone;
 }
 
 // Device-side view of the metadata in the workspace.
@@ -591,10 +596,14 @@ __device__ __forceinline__ float fast_rcp(float x) {
 __device__ __forceinline__ float capped_far(const ScoreMods& m, float raw) {
   return m.cap2 - 2.f * m.cap2 * fast_rcp(1.f + fast_exp2(raw * m.cap_k));
 }
+// The polynomial: the capped score is raw times it (UNIT: m.unit is not 1).
+template <bool UNIT>
+__device__ __forceinline__ float cap_poly(const ScoreMods& m, float raw) {
+  const float v = UNIT ? raw * m.unit : raw, u = v * v;
+  return fmaf(fmaf(fmaf(u, m.q[3], m.q[2]), u, m.q[1]), u, m.q[0]);
+}
 __device__ __forceinline__ float capped_score(const ScoreMods& m, float raw) {
-  const float v = raw * m.unit, u = v * v;
-  const float p = fmaf(fmaf(fmaf(m.q[3], u, m.q[2]), u, m.q[1]), u, m.q[0]);
-  return fabsf(raw) <= m.near ? raw * p : capped_far(m, raw);
+  return fabsf(raw) <= m.near ? raw * cap_poly<true>(m, raw) : capped_far(m, raw);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -782,6 +791,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The same, before any use of r[0..31].
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]));
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 }  // namespace pkv
