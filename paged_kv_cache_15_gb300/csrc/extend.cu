@@ -36,6 +36,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -80,6 +82,13 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 }
 
 constexpr uint32_t kNegInfBits = 0xff800000u;
+
+// Caps (times log2 e) up to which the quotient form alone is exact enough: its
+// error of 2^-22 cap2 moves no weight by more than 2e-5.
+constexpr float kQuotientCap2 = 100.f;
+enum ScoreForm : int { kLinear, kPoly, kQuotient, kEither };
+template <int F>
+using Form = std::integral_constant<int, F>;
 
 // 32-byte global store (sm_100+): a whole sector per lane, half the store
 // instructions of 16-byte vectors. The address must be 32-byte aligned.
@@ -965,6 +974,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
       // l: the row's running sum of p
       float m_ref = 0.f, l = 0.f;
       bool aborted = false;
+      // the form of the scores: the polynomial until a key leaves its range
+      const int far_form = a.mods.cap2 > kQuotientCap2 ? kEither : kQuotient;
+      int how = a.mods.cap2 == 0.f ? kLinear : kPoly;
       // the cap's coefficients as register pairs (opaque: the compiler would
       // fetch them anew at every use)
       uint64_t cap_q[4] = {0, 0, 0, 0};
@@ -1032,77 +1044,71 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         };
         // Scores with a cap or bias: 32 raw ones (keys from key0 + 32 cc) become
         // their log2-domain values less the reference (nref = -m_ref), masked
-        // keys -inf. The cap is taken by its polynomial, the largest |raw| kept on
-        // the way (keys behind the row's limit, which may hold anything, at worst
-        // cost a second pass); where that leaves the polynomial's range the
-        // tile's pass runs again with exact set, which picks the polynomial or
-        // the quotient key by key. Packed operations with the coefficients in
-        // registers: the pass is straight-line code of some 700 instructions for
-        // two warps a scheduler, and bound by their number.
+        // keys -inf. The cap is taken by its polynomial (kPoly), the largest |raw|
+        // kept on the way (keys behind the row's limit, which may hold anything,
+        // at worst cost a second pass); where that leaves the polynomial's range
+        // the pass runs again by the quotient, whose error of 2^-22 cap2 does not
+        // count up to kQuotientCap2 (kQuotient), beyond that by whichever of the
+        // two fits each key (kEither). how keeps to those while the scores stay
+        // large, so a head with large scores does not pay twice.
+        // Packed operations with the coefficients in registers, and no branch
+        // between the scores and their exponentials: the FMA and exponential
+        // units then work side by side (prefix-cached extend of 8 requests with
+        // a cap of 50: 571 us, with such a branch 683; 329 us without a cap).
         float big = 0.f;
-        auto scores32 = [&](int cc, uint32_t* sr, float nref, bool exact) {
+        auto scores32 = [&](auto form, int cc, uint32_t* sr, float nref) {
+          constexpr int F = decltype(form)::value;
           const float base = EXTRAS == kExtrasBias ? fmaf(slope, (float)(key0 + cc * 32 - limit), nref) : nref;
-          if (exact) {
+          // biases of eight keys, eight slopes further each time
+          uint64_t b[4] = {f2_pack(base, base), 0, 0, 0};
+          if constexpr (EXTRAS == kExtrasBias) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float r = __uint_as_float(sr[i]);
-              const float t = EXTRAS == kExtrasBias && a.mods.cap2 == 0.f ? r * a.scale_log2 : capped_score(a.mods, r);
-              sr[i] = __float_as_uint(t + (EXTRAS == kExtrasBias ? fmaf(slope, (float)i, base) : base));
-            }
-          } else {
-            // biases of eight keys, eight slopes further each time
-            uint64_t b[4] = {f2_pack(base, base), 0, 0, 0};
+            for (int k = 0; k < 4; ++k)
+              b[k] = f2_pack(fmaf(slope, (float)(2 * k), base), fmaf(slope, (float)(2 * k + 1), base));
+          }
+          const uint64_t eight = f2_pack(8.f * slope, 8.f * slope);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float r0 = __uint_as_float(sr[i]), r1 = __uint_as_float(sr[i + 1]);
+            const uint64_t raw = f2_pack(r0, r1);
+            uint64_t add = b[0];
             if constexpr (EXTRAS == kExtrasBias) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                b[k] = f2_pack(fmaf(slope, (float)(2 * k), base), fmaf(slope, (float)(2 * k + 1), base));
+              add = b[(i >> 1) & 3];
+              b[(i >> 1) & 3] = f2_add(add, eight);
             }
-            const uint64_t eight = f2_pack(8.f * slope, 8.f * slope);
-            auto bias = [&](int i) {
-              if constexpr (EXTRAS != kExtrasBias) return b[0];
-              const uint64_t now = b[(i >> 1) & 3];
-              b[(i >> 1) & 3] = f2_add(now, eight);
-              return now;
-            };
-            if (EXTRAS == kExtrasBias && a.mods.cap2 == 0.f) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const uint64_t t = f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sc2, bias(i));
-                sr[i] = __float_as_uint(f2_lo(t));
-                sr[i + 1] = __float_as_uint(f2_hi(t));
-              }
+            if constexpr (F != kLinear) big = max3f(big, fabsf(r0), fabsf(r1));
+            uint64_t t;
+            if constexpr (F == kLinear) {
+              t = f2_fma(raw, sc2, add);
+            } else if constexpr (F == kPoly) {
+              const uint64_t v = C::FP4 ? f2_mul(raw, f2_pack(a.mods.unit, a.mods.unit)) : raw;
+              const uint64_t u = f2_mul(v, v);
+              const uint64_t p = f2_fma(f2_fma(f2_fma(cap_q[3], u, cap_q[2]), u, cap_q[1]), u, cap_q[0]);
+              t = f2_fma(raw, p, add);
+            } else if constexpr (F == kQuotient) {
+              t = f2_add(f2_pack(capped_far(a.mods, r0), capped_far(a.mods, r1)), add);
             } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float r0 = __uint_as_float(sr[i]), r1 = __uint_as_float(sr[i + 1]);
-                big = max3f(big, fabsf(r0), fabsf(r1));
-                const uint64_t raw = f2_pack(r0, r1);
-                const uint64_t v = C::FP4 ? f2_mul(raw, f2_pack(a.mods.unit, a.mods.unit)) : raw;
-                const uint64_t u = f2_mul(v, v);
-                const uint64_t p = f2_fma(f2_fma(f2_fma(cap_q[3], u, cap_q[2]), u, cap_q[1]), u, cap_q[0]);
-                const uint64_t t = f2_fma(raw, p, bias(i));
-                sr[i] = __float_as_uint(f2_lo(t));
-                sr[i + 1] = __float_as_uint(f2_hi(t));
-              }
+              t = f2_add(f2_pack(capped_score(a.mods, r0), capped_score(a.mods, r1)), add);
             }
+            sr[i] = __float_as_uint(f2_lo(t));
+            sr[i + 1] = __float_as_uint(f2_hi(t));
           }
           if (diag) mask32_bits(sr, visible32(key0 + cc * 32, limit, draft0, tword));
         };
         // P of the tile against the reference; returns the tile's row sum
-        auto exp_pass = [&](bool exact) {
+        auto exp_pass = [&](auto form) {
           const uint64_t nref2 = f2_pack(-m_ref, -m_ref);
           uint64_t acc[4] = {0, 0, 0, 0};
           if constexpr (kScores) {
-            // 32 columns at a time, the next 32 on their way meanwhile
-            uint32_t sr[2][32];
-            tmem_ld32(lane_base + s_col, sr[0]);
-            tmem_wait_ld32(sr[0]);
+            // 32 columns at a time (64, or the next 32 requested ahead, cost
+            // registers that the coefficients want: 620 and 588 us against 571)
 #pragma unroll
             for (int cc = 0; cc < kExtendKeys / 32; ++cc) {
-              if (cc + 1 < kExtendKeys / 32) tmem_ld32(lane_base + s_col + (cc + 1) * 32, sr[(cc + 1) & 1]);
-              scores32(cc, sr[cc & 1], -m_ref, exact);
-              exp32<C::CODED, true>(sr[cc & 1], sc2, nref2, pk + cc * 16, acc);
-              if (cc + 1 < kExtendKeys / 32) tmem_wait_ld32(sr[(cc + 1) & 1]);
+              uint32_t sr[32];
+              tmem_ld32(lane_base + s_col + cc * 32, sr);
+              tmem_wait_ld();
+              scores32(form, cc, sr, -m_ref);
+              exp32<C::CODED, true>(sr, sc2, nref2, pk + cc * 16, acc);
             }
           } else {
 #pragma unroll
@@ -1116,9 +1122,22 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
           const uint64_t accs = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
           return f2_lo(accs) + f2_hi(accs);
         };
-        float tsum = exp_pass(false);
+        float tsum;
         if constexpr (kScores) {
-          if (__any_sync(0xffffffffu, a.mods.cap2 != 0.f && !(big <= a.mods.near))) tsum = exp_pass(true);
+          if (how == kPoly) {
+            big = 0.f;
+            tsum = exp_pass(Form<kPoly>{});
+            if (__any_sync(0xffffffffu, !(big <= a.mods.near))) how = far_form;
+          }
+          if (how != kPoly) {
+            big = 0.f;
+            tsum = how == kLinear     ? exp_pass(Form<kLinear>{})
+                   : how == kQuotient ? exp_pass(Form<kQuotient>{})
+                                      : exp_pass(Form<kEither>{});
+            if (how != kLinear && __all_sync(0xffffffffu, big <= a.mods.near)) how = kPoly;
+          }
+        } else {
+          tsum = exp_pass(Form<kLinear>{});
         }
         // The tile sum bounds every p of the row: while it is at most 2^16 no p
         // can overflow bf16 P or the fp32 O and l, and the reference (which
@@ -1139,8 +1158,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
             for (int cc = 0; cc < kExtendKeys / 32; ++cc) {
               uint32_t sr[32];
               tmem_ld32(lane_base + s_col + cc * 32, sr);
-              tmem_wait_ld32(sr);
-              scores32(cc, sr, 0.f, true);
+              tmem_wait_ld();
+              if (a.mods.cap2 == 0.f)
+                scores32(Form<kLinear>{}, cc, sr, 0.f);
+              else
+                scores32(Form<kEither>{}, cc, sr, 0.f);
               mx = max32(sr, mx);
             }
           } else {
@@ -1172,7 +1194,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
             l *= alpha;
             m_ref = mt;
           }
-          tsum = exp_pass(true);
+          if (kScores && a.mods.cap2 != 0.f)
+            tsum = exp_pass(Form<kEither>{});
+          else
+            tsum = exp_pass(Form<kLinear>{});
         }
         // P overwrites the first half of this tile's S columns
         tmem_st32(lane_base + s_col, pk);
