@@ -1160,14 +1160,8 @@ int run_decode(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   // L2 fills no wider than one head's row of an E4M3 pool (128 bytes)
   const CUtensorMapL2promotion promo = C::FP8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   if (C::FP4) {
-    // one row a tile, as 8-byte words (a box holds at most 256 elements)
-    const uint64_t rows = slots / kSegSlots * (uint64_t)c.cfg.num_kv_heads;
-    const uint32_t words = fp4_tile_bytes(C::DK) / 8;
-    if (rows >= 0x7fffffffull) return PKV_ERR_UNSUPPORTED;
-    if (encode_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, const_cast<void*>(k_pool), words, rows, words * 8, words, 1,
-                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) != PKV_OK ||
-        encode_tmap_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, const_cast<void*>(v_pool), words, rows, words * 8, words, 1,
-                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) != PKV_OK)
+    if (encode_tmap_fp4(&tk, k_pool, C::DK, c.cfg.num_kv_heads, slots) != PKV_OK ||
+        encode_tmap_fp4(&tv, v_pool, C::DV, c.cfg.num_kv_heads, slots) != PKV_OK)
       return PKV_ERR_CUDA;
   } else if (encode_tmap_2d(&tk, dt, const_cast<void*>(k_pool), inner_k, slots, inner_k * C::kElem, box_inner,
                             kSegSlots, CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK ||

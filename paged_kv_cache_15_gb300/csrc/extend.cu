@@ -229,6 +229,7 @@ __device__ __forceinline__ UnitKV unit_kv(const ExtendTile& u, bool rev) {
 // the codes into raw rings (RK / RV tiles), the K and V producer warps widen
 // them to f16 (exactly; 4-bit codes times their block scales) into the operand
 // rings, and the MMAs run in f16 with Q and P rounded to f16.
+constexpr int kFp4HalfSegs = 4;
 template <int DK_, int DV_, int NK_, int NV_, int KV_ = PKV_KV_BF16, int RK_ = 0, int RV_ = 0>
 struct ExtCfg {
   static constexpr int DK = DK_;
@@ -252,8 +253,9 @@ struct ExtCfg {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = 2 * kQBytes;
   static constexpr int kVOff = kKOff + NK * kTileBytesK;
-  // 128 E4M3 codes per row, or the pool's 16-slot tiles of 4-bit codes
-  static constexpr int kRawTileBytes = FP4 ? kExtendKeys / kSegSlots * fp4_tile_bytes(DK) : kExtendKeys * 128;
+  // raw slots: a tile of 128 E4M3 codes a row, or half a tile (four of the
+  // pool's 16-slot tiles) of 4-bit codes
+  static constexpr int kRawTileBytes = FP4 ? kFp4HalfSegs * fp4_tile_bytes(DK) : kExtendKeys * 128;
   static constexpr int kRawKOff = kVOff + NV * kTileBytesV;
   static constexpr int kRawVOff = kRawKOff + RK * kRawTileBytes;
   static constexpr int kBarOff = kRawVOff + RV * kRawTileBytes;
@@ -286,7 +288,6 @@ struct ExtendArgs {
   // path's verify shapes (at most 128 rows per KV head); 0: the extend plan
   int dplan;
   ScoreMods mods;  // score cap and distance bias (kExtrasCap, kExtrasBias)
-  const uint8_t *k_pool, *v_pool;  // the pools' bytes (4-bit pools: bulk copies of their tiles)
 };
 
 // Work unit idx of the plan the kernel runs. A decode-plan item (request b,
@@ -404,20 +405,188 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
     return a.q_tma != 0 && a.m.qo_indptr[u.b] + (u.row0 + x * kExtendRows) / G + a.q_box_tokens <= total_q;
   };
 
-  if (C::CODED && (warp == C::kProducerWarp || warp == C::kVProducerWarp)) {
-    // ------------------------------------------------------------ producers of coded pools
+  if (C::FP4 && (warp == C::kProducerWarp || warp == C::kVProducerWarp)) {
+    // ------------------------------------------------------------ producers of 4-bit pools
+    // As the E4M3 producers below, with raw slots of half a tile: one gather
+    // brings four of the pool's 16-slot tiles (segments past the request's end
+    // point outside the map and come as zeros), and with three slots a stream
+    // the next two halves are on their way while one is widened. (One whole
+    // tile in flight left its latency open on every tile: 707 us against FIGFP4
+    // on the prefix-cached extend of 8 requests.)
+    const bool is_v = warp == C::kVProducerWarp;
+    const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
+    if (elect_one()) prefetch_tmap(tmap);
+    const int R = is_v ? C::RV : C::RK;
+    const int depth = is_v ? NV : NK;
+    uint64_t* rfull = is_v ? raw_full + C::RK : raw_full;
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
+    uint8_t* raw_ring = smem + (is_v ? C::kRawVOff : C::kRawKOff);
+    const uint32_t raw_base = smem_u32(raw_ring);
+    const uint32_t op_base = smem_u32(smem + (is_v ? C::kVOff : C::kKOff));
+    constexpr int kOpTile = kExtendKeys * 128 * 2;  // one f16 tile of 128-wide rows
+    constexpr int kSegBytes = fp4_tile_bytes(DK);
+    const uint64_t pol_stream = policy_evict_first();  // the bf16 producers' choice, below
+    const uint64_t pol_reuse = policy_evict_normal();
+    uint32_t jt = 0;            // operand tiles so far
+    uint32_t rt = 0, ct = 0;    // halves requested / widened so far
+    uint32_t rslot = 0, cslot = 0, cphase = 0;  // their slots, and the phase of the next to widen
+    uint32_t qcount[2] = {0, 0}, qtcount[2] = {0, 0};
+    bool stop = false;
+    const int c = lane & 7, r0 = lane >> 3;  // block of 16 codes and first row of this lane
+    const bool hold_first = !is_v && blockIdx.x == 0 && __ldcg(plan + kHoldLoad) != 0;
+    for (int w = blockIdx.x; w < n_units && !stop; w += gridDim.x) {
+      const ExtendTile u = load_unit(a, w / a.num_kv_heads);
+      const int g = w % a.num_kv_heads;
+      const UnitKV ukv = unit_kv(u, rev);
+      const int np = a.m.seg_indptr[u.b + 1] - a.m.seg_indptr[u.b];
+      const int page_base = a.m.seg_indptr[u.b];
+      const bool reused = !a.dplan && (a.m.qo_indptr[u.b + 1] - a.m.qo_indptr[u.b]) * G > kExtendUnitRows;
+      const uint64_t pol = reused ? pol_reuse : pol_stream;
+      auto seq_tile = [&](int e) {
+        if (!ukv.dual) return ukv.s0 + (rev ? ukv.len() - 1 - e : e);
+        const int m = min(ukv.n0, ukv.n1);
+        const int step = e < 2 * m ? e >> 1 : e - m;
+        const int x = e < 2 * m ? (e & 1) : (ukv.n0 > ukv.n1 ? 0 : 1);
+        return ukv.tile(x, step);
+      };
+      const int len = ukv.len();
+      // map rows of 4 consecutive tiles' segments: lane 8k + p holds segment p of tile e0 + k
+      auto load_group = [&](int e0) {
+        const int e = e0 + (lane >> 3), p = lane & 7;
+        if (e >= len) return 0x7fffffff;
+        const int jj = seq_tile(e);
+        return p < np - jj * kPagesPerTile
+                   ? __ldg(a.m.seg_indices + page_base + jj * kPagesPerTile + p) * a.num_kv_heads + g
+                   : 0x7fffffff;
+      };
+      int grp = load_group(0);
+      int grp_next = load_group(4);
+      int issued = 0;  // halves of this unit requested
+      auto issue = [&]() {
+        const int e = issued >> 1;
+        if (e > 0 && (issued & 7) == 0) {
+          grp = grp_next;
+          grp_next = load_group(e + 4);
+        }
+        const int at = ((e & 3) << 3) + (issued & 1) * kFp4HalfSegs;
+        const int y0 = __shfl_sync(0xffffffffu, grp, at), y1 = __shfl_sync(0xffffffffu, grp, at + 1);
+        const int y2 = __shfl_sync(0xffffffffu, grp, at + 2), y3 = __shfl_sync(0xffffffffu, grp, at + 3);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&rfull[rslot], (uint32_t)C::kRawTileBytes);
+          if (!(hold_first && rt == 0))
+            tma_gather4_hint(raw_ring + rslot * C::kRawTileBytes, tmap, 0, y0, y1, y2, y3, &rfull[rslot], pol);
+        }
+        ++rt;
+        ++issued;
+        if (++rslot == (uint32_t)R) rslot = 0;
+      };
+      for (int k = 0; k < R && issued < 2 * len; ++k) issue();
+      if (!is_v) {
+        // Q of the unit, as the E4M3 producers hand it over
+        for (int x = 0; x < 2 && !stop; ++x) {
+          if (!ukv.uses_q(x)) continue;
+          if (!mbar_wait_warp(&q_empty[x], (qcount[x] & 1) ^ 1, plan, s_abort) ||
+              !mbar_wait_warp(&q_written[x], qtcount[x] & 1, plan, s_abort)) {
+            stop = true;
+            break;
+          }
+          ++qtcount[x];
+          ++qcount[x];
+          if (elect_one()) mbar_arrive(&q_full[x]);
+        }
+        if (stop) break;
+      }
+      for (int e = 0; e < len && !stop; ++e, ++jt) {
+        const int st = jt % depth;
+        if (!mbar_wait_warp(&empty[st], ((jt / depth) & 1) ^ 1, plan, s_abort)) {
+          stop = true;
+          break;
+        }
+        for (int part = 0; part < 2; ++part) {
+          if (!mbar_wait_warp(&rfull[cslot], cphase, plan, s_abort)) {
+            stop = true;
+            break;
+          }
+          const uint32_t src = raw_base + cslot * C::kRawTileBytes;
+          ++ct;
+          if (++cslot == (uint32_t)R) {
+            cslot = 0;
+            cphase ^= 1;
+          }
+          // lane: block c of rows r0 + 4k; 8 bytes and the block's scale in,
+          // f16 chunks 2c and 2c + 1 of column block c / 4 out
+          const uint32_t out_blk =
+              op_base + st * kOpTile + (c >> 2) * (kExtendKeys * 128) + part * (kFp4HalfSegs * kSegSlots * 128);
+          const uint32_t codes = src + r0 * 64 + c * 8, scales = src + kSegSlots * 64 + r0 * 8 + c;
+          auto ld = [&](int k, uint2& x, uint16_t& sc) {  // (row r0 + 4k: segment k / 4, row 4 * (k % 4) + r0)
+            const uint32_t at = (k >> 2) * kSegBytes;
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(codes + at + (k & 3) * 256));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=h"(sc) : "r"(scales + at + (k & 3) * 32));
+          };
+          auto widen = [&](int k, const uint2& x, uint16_t sc) {
+            const int r = r0 + 4 * k;
+            const uint32_t s2 = e4m3x2_to_f16x2(sc);
+            uint32_t v[8];
+            e2m1x8_to_f16x2(x.x, v);
+            e2m1x8_to_f16x2(x.y, v + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = mul_f16x2_by<false>(v[i], s2);  // exact: at most 6 significant bits
+            const uint32_t row = out_blk + r * 128;
+            sts128(row + ((((2 * c) & 7) ^ (r & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+            sts128(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4), make_uint4(v[4], v[5], v[6], v[7]));
+          };
+          // four rows a lane in flight, the next four loaded before they are widened
+          uint2 x[4];
+          uint16_t sc[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) ld(v, x[v], sc[v]);
+#pragma unroll
+          for (int k0 = 0; k0 < 16; k0 += 4) {
+            uint2 y[4];
+            uint16_t ysc[4];
+            if (k0 + 4 < 16) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) ld(k0 + 4 + v, y[v], ysc[v]);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) widen(k0 + v, x[v], sc[v]);
+            if (k0 + 4 < 16) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) x[v] = y[v], sc[v] = ysc[v];
+            }
+          }
+          // the f16 tile is read by the tensor core (async proxy), and the raw
+          // slot is refilled by TMA next
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (issued < 2 * len) issue();
+        }
+        if (!stop && lane == 0) mbar_arrive(&full[st]);
+      }
+    }
+    if (stop && lane == 0) *s_abort = 1;
+    // never leave the CTA with a TMA still writing into shared memory (these
+    // waits ignore the abort flag on purpose)
+    for (; ct < rt; ++ct) {
+      mbar_wait(&rfull[cslot], cphase, plan);
+      if (++cslot == (uint32_t)R) {
+        cslot = 0;
+        cphase ^= 1;
+      }
+    }
+    __syncwarp();
+  } else if (C::CODED && (warp == C::kProducerWarp || warp == C::kVProducerWarp)) {
+    // ------------------------------------------------------------ E4M3 producers
     // Warp 8 streams K, warp 10 V. TMA lands each tile's codes in the raw ring
-    // (E4M3: one 16-row x 128-byte box per page, 128-byte swizzle; 4-bit: one
-    // bulk copy per 16-slot tile, as it lies in the pool); the warp widens
+    // (one 16-row x 128-byte box per page, 128-byte swizzle); the warp widens
     // the rows of the loaded pages to f16 (exact) into the operand ring, in
     // the operand layout (two 64-column blocks, 128-byte swizzle), and marks
     // the operand tile full. A raw slot is requested again as soon as the warp
     // has read it, R tiles ahead of the widening. Warp 8 also hands Q over.
     const bool is_v = warp == C::kVProducerWarp;
     const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
-    const uint8_t* pool = is_v ? a.v_pool : a.k_pool;
-    constexpr int kSegBytes = C::FP4 ? fp4_tile_bytes(DK) : kSegSlots * 128;  // raw bytes of 16 slots
-    if (!C::FP4 && elect_one()) prefetch_tmap(tmap);
+    if (elect_one()) prefetch_tmap(tmap);
     const int R = is_v ? C::RV : C::RK;
     const int depth = is_v ? NV : NK;
     uint64_t* rfull = is_v ? raw_full + C::RK : raw_full;
@@ -473,21 +642,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         const int npg = min(kPagesPerTile, np - j * kPagesPerTile);
         const int rs = (int)(rt % R);
         const bool leader = elect_one();
-        if (leader) mbar_arrive_expect_tx(&rfull[rs], (uint32_t)(npg * kSegBytes));
+        if (leader) mbar_arrive_expect_tx(&rfull[rs], (uint32_t)(npg * kSegSlots * 128));
         uint8_t* dst = raw_ring + rs * C::kRawTileBytes;
-        if constexpr (C::FP4) {
-          __syncwarp();
-          const int pg = __shfl_sync(0xffffffffu, grp, ((e & 3) << 3) + (lane & 7));
-          if (lane < npg && !(hold_first && rt == 0))
-            bulk_load_hint(dst + lane * kSegBytes, pool + ((long long)pg * a.num_kv_heads + g) * kSegBytes, kSegBytes,
-                           &rfull[rs], pol);
-        } else {
 #pragma unroll
-          for (int p = 0; p < kPagesPerTile; ++p) {
-            const int pg = __shfl_sync(0xffffffffu, grp, ((e & 3) << 3) + p);
-            if (p < npg && leader && !(hold_first && rt == 0))
-              tma_load_2d_hint(dst + p * kSegBytes, tmap, g * 128, pg * kSegSlots, &rfull[rs], pol);
-          }
+        for (int p = 0; p < kPagesPerTile; ++p) {
+          const int pg = __shfl_sync(0xffffffffu, grp, ((e & 3) << 3) + p);
+          if (p < npg && leader && !(hold_first && rt == 0))
+            tma_load_2d_hint(dst + p * (kSegSlots * 128), tmap, g * 128, pg * kSegSlots, &rfull[rs], pol);
         }
         ++rt;
         ++issued;
@@ -527,38 +688,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
         const uint32_t src = raw_base + rs * C::kRawTileBytes;
         const uint32_t out_blk = op_base + st * kOpTile + (c >> 2) * (kExtendKeys * 128);
         // lane: chunk c (codes 16c .. 16c + 15) of rows r0 + 4k; one 16-byte
-        // chunk in (4-bit: 8 bytes and the block's scale), f16 chunks 2c and
-        // 2c + 1 of column block c / 4 out. Four rows a group, the next
-        // group's chunks loaded before this one is widened.
+        // chunk in, f16 chunks 2c and 2c + 1 of column block c / 4 out. Four
+        // rows a group, the next group's chunks loaded before this one is widened.
         auto ld = [&](int k) {
           const int r = r0 + 4 * k;
-          if constexpr (C::FP4) {
-            const uint32_t seg = src + (r / kSegSlots) * kSegBytes;
-            const int i = r % kSegSlots;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            uint16_t s;
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(seg + i * 64 + c * 8));
-            asm volatile("ld.shared.u8 %0, [%1];" : "=h"(s) : "r"(seg + kSegSlots * 64 + i * 8 + c));
-            x.z = s;
-            return x;
-          } else {
-            return lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
-          }
+          return lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
         };
         auto widen = [&](int k, const uint4& x) {
           const int r = r0 + 4 * k;
-          if constexpr (C::FP4) {
-            const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(x.z | (x.z << 8)));
-            uint32_t w[8];
-            e2m1x8_to_f16x2(x.x, w);
-            e2m1x8_to_f16x2(x.y, w + 4);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = mul_f16x2(w[i], s2);  // exact: at most 6 significant bits
-            const uint32_t row = out_blk + r * 128;
-            sts128(row + ((((2 * c) & 7) ^ (r & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
-            sts128(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4), make_uint4(w[4], w[5], w[6], w[7]));
-            return;
-          }
           const uint4 lo = make_uint4(e4m3x2_to_f16x2((uint16_t)(x.x & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(x.x >> 16)),
                                       e4m3x2_to_f16x2((uint16_t)(x.y & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(x.y >> 16)));
           const uint4 hi = make_uint4(e4m3x2_to_f16x2((uint16_t)(x.z & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(x.z >> 16)),
@@ -1358,13 +1495,16 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   const uint32_t esz = C::CODED ? 1 : 2;
   // L2 fills no wider than one head's row of an E4M3 pool (128 bytes)
   const CUtensorMapL2promotion promo = C::CODED ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-  // (4-bit tiles come by untiled bulk copies)
-  if (!C::FP4 && encode_tmap_2d(&tk, dt, const_cast<void*>(k_pool), inner_k, slots, inner_k * esz, 128 / esz, kSegSlots,
-                                CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
+  if (C::FP4) {
+    if (encode_tmap_fp4(&tk, k_pool, C::DK, c.cfg.num_kv_heads, slots) != PKV_OK ||
+        encode_tmap_fp4(&tv, v_pool, C::DV, c.cfg.num_kv_heads, slots) != PKV_OK)
+      return PKV_ERR_CUDA;
+  } else if (encode_tmap_2d(&tk, dt, const_cast<void*>(k_pool), inner_k, slots, inner_k * esz, 128 / esz, kSegSlots,
+                            CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK ||
+             encode_tmap_2d(&tv, dt, const_cast<void*>(v_pool), inner_v, slots, inner_v * esz, 128 / esz, kSegSlots,
+                            CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK) {
     return PKV_ERR_CUDA;
-  if (!C::FP4 && encode_tmap_2d(&tv, dt, const_cast<void*>(v_pool), inner_v, slots, inner_v * esz, 128 / esz, kSegSlots,
-                     CU_TENSOR_MAP_SWIZZLE_128B, promo) != PKV_OK)
-    return PKV_ERR_CUDA;
+  }
   ExtendArgs a;
   a.m = make_meta(c);
   a.q = static_cast<const uint16_t*>(q);
@@ -1378,8 +1518,6 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
   a.scale_log2 = sm_scale * (C::CODED ? k_scale : 1.f) * kLog2e;
   a.v_scale = C::CODED ? v_scale : 1.f;
   a.mods = score_mods(c, a.scale_log2);
-  a.k_pool = static_cast<const uint8_t*>(k_pool);
-  a.v_pool = static_cast<const uint8_t*>(v_pool);
   a.out_32B = (reinterpret_cast<uintptr_t>(out) & 31) == 0 ? 1 : 0;
   a.tree = active_tree(c);
   a.sinks = c.sinks;
@@ -1423,9 +1561,9 @@ int run_extend(Ctx& c, const void* q, const void* k_pool, const void* v_pool, fl
 int run_tc(Ctx& c, const void* q, const void* k_pool, const void* v_pool, float sm_scale, float k_scale,
            float v_scale, void* out, float* lse, cudaStream_t st, bool dplan) {
   if (c.cfg.kv_dtype == PKV_KV_FP4_E2M1) {
-    // 4-bit pools: raw tiles of 9 KB, two K tiles and one V tile in flight
+    // 4-bit pools: three raw halves of 4.5 KB in flight for each of K and V
     if (c.cfg.head_dim != 128) return PKV_ERR_UNSUPPORTED;
-    return run_extend<ExtCfg<128, 128, 2, 2, PKV_KV_FP4_E2M1, 2, 1>>(c, q, k_pool, v_pool, sm_scale, k_scale, v_scale,
+    return run_extend<ExtCfg<128, 128, 2, 2, PKV_KV_FP4_E2M1, 3, 3>>(c, q, k_pool, v_pool, sm_scale, k_scale, v_scale,
                                                                      out, lse, st, dplan);
   }
   if (c.cfg.kv_dtype == PKV_KV_FP8_E4M3) {

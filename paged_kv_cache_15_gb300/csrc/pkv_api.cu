@@ -42,6 +42,8 @@ int check_config(const pkv_config* cfg) {
   // slot indices and pool element offsets must fit the kernels' index types
   const long long slots = (long long)cfg->num_pages * cfg->page_size;
   if (slots > (1ll << 31) - 1) return PKV_ERR_UNSUPPORTED;
+  if (cfg->kv_dtype == PKV_KV_FP4_E2M1 && slots / kSegSlots * cfg->num_kv_heads >= (1ll << 31) - 1)
+    return PKV_ERR_UNSUPPORTED;
   if ((long long)cfg->max_q_tokens * cfg->num_q_heads * dk > (1ll << 40)) return PKV_ERR_UNSUPPORTED;
   // segment counts (pages times segments per page) must fit an int
   if ((long long)cfg->max_pages_total * (cfg->page_size / kSegSlots) > (1ll << 30)) return PKV_ERR_UNSUPPORTED;
@@ -199,6 +201,13 @@ int encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, void* base, uint
   CUresult r = g_encode(map, dtype, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, promo,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int encode_tmap_fp4(CUtensorMap* map, const void* pool, int width, int heads, uint64_t slots) {
+  const uint32_t words = fp4_tile_bytes(width) / 8;
+  return encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, const_cast<void*>(pool), words,
+                        slots / kSegSlots * (uint64_t)heads, (uint64_t)words * 8, words, 1,
+                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
 int encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, void* base, uint64_t d0, uint64_t d1, uint64_t d2,
