@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
     // brings four of the pool's 16-slot tiles (segments past the request's end
     // point outside the map and come as zeros), and with three slots a stream
     // the next two halves are on their way while one is widened. (One whole
-    // tile in flight left its latency open on every tile: 707 us against FIGFP4
+    // tile in flight left its latency open on every tile: 707 us against 550
     // on the prefix-cached extend of 8 requests.)
     const bool is_v = warp == C::kVProducerWarp;
     const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;

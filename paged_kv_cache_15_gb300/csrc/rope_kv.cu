@@ -23,6 +23,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr long long kStreamBytes = 128ll << 20;  // rows read and written by a launch
 
 enum Rot { kRotNone = 0, kRotHalf = 1, kRotInterleaved = 2 };
 
@@ -81,11 +82,23 @@ __device__ __forceinline__ uint2 quant_fp4(const float* y, uint8_t* scale) {
 }
 
 // 16 bytes of an input row; volatile, so that it stays ahead of the loads whose
-// chain it is to overlap.
+// chain it is to overlap. STREAM: read and written once, out of the L2's way.
+template <bool STREAM>
 __device__ __forceinline__ uint4 load_row(const uint16_t* p) {
   uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  if constexpr (STREAM)
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  else
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
+}
+
+template <bool STREAM, typename T>
+__device__ __forceinline__ void store(T* p, const T& v) {
+  if constexpr (STREAM)
+    __stcs(p, v);
+  else
+    *p = v;
 }
 
 struct RopeKvArgs {
@@ -106,15 +119,15 @@ struct RopeKvArgs {
 
 // Row `head` of width D at a slot (or token): 16 columns (block cb) stored as
 // bf16, or scaled and rounded to the pool's codes.
-template <int D>
+template <int D, bool STREAM>
 __device__ __forceinline__ void store_bf16(void* rows, long long slot, int heads, int head, int cb, const uint4& x0,
                                            const uint4& x1) {
   uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(rows) + (slot * heads + head) * D + cb * 16);
-  dst[0] = x0;
-  dst[1] = x1;
+  store<STREAM>(dst, x0);
+  store<STREAM>(dst + 1, x1);
 }
 
-template <int D, int KV>
+template <int D, int KV, bool STREAM>
 __device__ __forceinline__ void store_coded(void* pool, long long slot, int heads, int head, int cb, const float* x,
                                             float inv) {
   float y[16];
@@ -125,8 +138,8 @@ __device__ __forceinline__ void store_coded(void* pool, long long slot, int head
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       w[i] = (uint32_t)e4m3x2(y[4 * i], y[4 * i + 1]) | ((uint32_t)e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(pool) + (slot * heads + head) * D + cb * 16) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+    store<STREAM>(reinterpret_cast<uint4*>(static_cast<uint8_t*>(pool) + (slot * heads + head) * D + cb * 16),
+                  make_uint4(w[0], w[1], w[2], w[3]));
   } else {
     uint8_t s;
     const uint2 codes = quant_fp4(y, &s);
@@ -137,13 +150,94 @@ __device__ __forceinline__ void store_coded(void* pool, long long slot, int head
   }
 }
 
-template <int DK, int DV, int KV, int ROT, int RPT>
+// The two 8-column vectors of a thread's 16 columns (block cb): whether they are
+// rotated, the column of their partners, their first angle, and whether the
+// partner's sine counts negative (the first half of the half-split pairing).
+template <int ROT>
+struct Where {
+  int partner[2], angle[2];
+  bool rot[2], low[2];
+  __device__ __forceinline__ Where(int cb, bool is_v, int first, int rotary) {
+    const int half = rotary / 2;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int col = cb * 16 + 8 * v, rel = col - first;
+      rot[v] = ROT != kRotNone && !is_v && rel >= 0 && rel < rotary;
+      low[v] = rel < half;
+      partner[v] = ROT == kRotHalf && rot[v] ? (low[v] ? col + half : col - half) : col;
+      angle[v] = ROT == kRotHalf ? (low[v] ? rel : rel - half) : rel / 2;
+    }
+  }
+};
+
+// Cosines and signed sines of those columns.
+template <int ROT>
+struct Angles {
+  float c[16], s[16];
+  // row: the position's cosines, then its sines (global or shared memory)
+  __device__ __forceinline__ void load(const Where<ROT>& w, const float* row, int half) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      if (!w.rot[v]) continue;
+      const float* at = row + w.angle[v];
+      if constexpr (ROT == kRotHalf) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 cc = *reinterpret_cast<const float4*>(at + i);
+          const float4 ss = *reinterpret_cast<const float4*>(at + half + i);
+          const float sg = w.low[v] ? -1.f : 1.f;  // (an exact change of sign)
+          c[8 * v + i] = cc.x, c[8 * v + i + 1] = cc.y, c[8 * v + i + 2] = cc.z, c[8 * v + i + 3] = cc.w;
+          s[8 * v + i] = sg * ss.x, s[8 * v + i + 1] = sg * ss.y, s[8 * v + i + 2] = sg * ss.z;
+          s[8 * v + i + 3] = sg * ss.w;
+        }
+      } else {
+        const float4 cc = *reinterpret_cast<const float4*>(at);
+        const float4 ss = *reinterpret_cast<const float4*>(at + half);
+        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          c[8 * v + 2 * i] = c[8 * v + 2 * i + 1] = cv[i];
+          s[8 * v + 2 * i] = -sv[i];
+          s[8 * v + 2 * i + 1] = sv[i];
+        }
+      }
+    }
+  }
+  // The rotated columns in fp32 (y) and as bf16 (out; columns that are not
+  // rotated keep their bits).
+  __device__ __forceinline__ void turn(const Where<ROT>& w, const uint4* own, const uint4* other, float* y,
+                                       uint4* out) const {
+    float x[16];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      out[v] = own[v];
+      widen8(own[v], x + 8 * v);
+      float p[8];
+      if constexpr (ROT == kRotHalf) {
+        widen8(other[v], p);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = x[8 * v + (e ^ 1)];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        y[8 * v + e] = w.rot[v] ? __fadd_rn(__fmul_rn(x[8 * v + e], c[8 * v + e]), __fmul_rn(p[e], s[8 * v + e]))
+                                : x[8 * v + e];
+      if (w.rot[v]) out[v] = narrow8(y + 8 * v);
+    }
+  }
+};
+
+template <int DK, int DV, int KV, int ROT, int RPT, bool STREAM>
 __global__ void __launch_bounds__(kThreads) rope_kv_kernel(RopeKvArgs a) {
   constexpr int CB = DK / 16;  // threads of a unit: 16 columns each
+  static_assert(KV == PKV_KV_BF16 || DK == DV, "coded pools: K and V heads of one width");
   pdl_launch_dependents();
   pdl_wait();
-  const long long t = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (t >= a.n_threads) return;
+  const long long thread = (long long)blockIdx.x * kThreads + threadIdx.x;
+  // (threads past the end repeat the last one's loads, for the exchange below)
+  const bool idle = thread >= a.n_threads;
+  const long long t = idle ? a.n_threads - 1 : thread;
   const int per_token = a.q_units + 2 * a.kv_units;
   const long long unit = t / CB;
   const int cb = (int)(t - unit * CB);
@@ -154,134 +248,91 @@ __global__ void __launch_bounds__(kThreads) rope_kv_kernel(RopeKvArgs a) {
   if (!is_q) u -= is_v ? a.q_units + a.kv_units : a.q_units;
   const int heads = is_q ? a.num_q_heads : a.num_kv_heads;
   const int h0 = u * RPT, h1 = min(heads, h0 + RPT);
-  if (is_v && cb * 16 >= DV) return;
+  const bool narrow = is_v && cb * 16 >= DV;  // past the end of a narrower V row
   // The rows are requested first, the token's position and slot after them:
   // the chain position -> angles then runs while the rows are on their way.
   const int width = is_v ? DV : DK;
   const uint16_t* src = (is_q   ? a.q + tok * a.q_stride
                          : is_v ? a.v + tok * a.v_stride
                                 : a.k + tok * a.k_stride);
-  // rotation of the two 8-column vectors of this thread: whether, partner
-  // column, first angle, sign of the sin term
   const int half = a.rotary / 2;
-  int partner[2], angle[2];
-  bool rot[2], low[2];
-#pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    const int col = cb * 16 + 8 * v, rel = col - a.first;
-    rot[v] = ROT != kRotNone && !is_v && rel >= 0 && rel < a.rotary;
-    low[v] = rel < half;
-    partner[v] = ROT == kRotHalf && rot[v] ? (low[v] ? col + half : col - half) : col;
-    angle[v] = ROT == kRotHalf ? (low[v] ? rel : rel - half) : rel / 2;
-  }
-  uint4 own[RPT][2], other[RPT][2];
+  const Where<ROT> where(cb, is_v, a.first, a.rotary);
+  // Partners of the half-split pairing are held by other threads of the row:
+  // where a row's threads lie in one warp they hand them over, else they are
+  // read a second time (from L1).
+  constexpr bool kExchange = ROT == kRotHalf && 32 % CB == 0;
+  uint4 own[RPT][2], other[kExchange ? 1 : RPT][2];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const uint16_t* row = src + min(h0 + i, h1 - 1) * width;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      own[i][v] = load_row(row + cb * 16 + 8 * v);
-      if (ROT == kRotHalf) other[i][v] = load_row(row + partner[v]);
+      own[i][v] = load_row<STREAM>(row + (narrow ? 0 : cb * 16 + 8 * v));
+      if (ROT == kRotHalf && !kExchange) other[i][v] = load_row<STREAM>(row + (narrow ? 0 : where.partner[v]));
     }
   }
   const int pos = ROT != kRotNone ? a.pos[tok] : 0;
   const long long slot = a.loc[tok];
+  bool live = !idle && !narrow;  // this thread stores
   if (ROT != kRotNone && (pos < 0 || pos >= a.max_pos)) {
-    if (cb == 0 && unit == tok * per_token) record_error(a.plan, PKV_DEV_BAD_POSITION, (int)tok);
-    return;
+    if (live && cb == 0 && unit == tok * per_token) record_error(a.plan, PKV_DEV_BAD_POSITION, (int)tok);
+    live = false;
+  } else if (!is_q && (slot < 0 || slot >= a.num_slots)) {
+    if (live && cb == 0 && u == 0 && !is_v) record_error(a.plan, PKV_DEV_BAD_SLOT, (int)tok);
+    live = false;
   }
-  if (!is_q && (slot < 0 || slot >= a.num_slots)) {
-    if (cb == 0 && u == 0 && !is_v) record_error(a.plan, PKV_DEV_BAD_SLOT, (int)tok);
-    return;
-  }
-  if (is_v) {
-#pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      const int h = h0 + i;
-      if (h >= h1) break;
-      if constexpr (KV == PKV_KV_BF16) {
-        store_bf16<DV>(a.v_pool, slot, heads, h, cb, own[i][0], own[i][1]);
-      } else {
-        float x[16];
-        widen8(own[i][0], x);
-        widen8(own[i][1], x + 8);
-        store_coded<DV, KV>(a.v_pool, slot, heads, h, cb, x, a.v_inv);
-      }
-    }
-    return;
-  }
-  float c[16], s[16];
-#pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    if (!rot[v]) continue;
-    const float* row = a.cos_sin + (long long)pos * a.rotary + angle[v];
-    if constexpr (ROT == kRotHalf) {
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 cc = *reinterpret_cast<const float4*>(row + i);
-        const float4 ss = *reinterpret_cast<const float4*>(row + half + i);
-        const float sg = low[v] ? -1.f : 1.f;  // (an exact change of sign)
-        c[8 * v + i] = cc.x, c[8 * v + i + 1] = cc.y, c[8 * v + i + 2] = cc.z, c[8 * v + i + 3] = cc.w;
-        s[8 * v + i] = sg * ss.x, s[8 * v + i + 1] = sg * ss.y, s[8 * v + i + 2] = sg * ss.z;
-        s[8 * v + i + 3] = sg * ss.w;
-      }
-    } else {
-      const float4 cc = *reinterpret_cast<const float4*>(row);
-      const float4 ss = *reinterpret_cast<const float4*>(row + half);
-      const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[8 * v + 2 * i] = c[8 * v + 2 * i + 1] = cv[i];
-        s[8 * v + 2 * i] = -sv[i];
-        s[8 * v + 2 * i + 1] = sv[i];
-      }
-    }
-  }
+  Angles<ROT> angles;
+  if (live) angles.load(where, a.cos_sin + (long long)pos * a.rotary, half);
+  const bool odd = (half / 8) & 1;  // the partner of one vector is then the other one elsewhere
+  const int lane0 = threadIdx.x & 31 & ~(CB - 1);
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int h = h0 + i;
-    if (h >= h1) break;
-    float x[16], y[16];
-    uint4 out[2];  // as bf16; columns that are not rotated keep their bits
+    uint4* partner = other[kExchange ? 0 : i];
+    if constexpr (kExchange) {
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      out[v] = own[i][v];
-      widen8(own[i][v], x + 8 * v);
-      float p[8];
-      if constexpr (ROT == kRotHalf) {
-        widen8(other[i][v], p);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = x[8 * v + (e ^ 1)];
+      for (int v = 0; v < 2; ++v) {
+        const int from = lane0 + (where.partner[v] >> 4);
+        const uint4 x = odd ? own[i][v ^ 1] : own[i][v];
+        partner[v] = make_uint4(__shfl_sync(0xffffffffu, x.x, from), __shfl_sync(0xffffffffu, x.y, from),
+                                __shfl_sync(0xffffffffu, x.z, from), __shfl_sync(0xffffffffu, x.w, from));
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        y[8 * v + e] = rot[v] ? __fadd_rn(__fmul_rn(x[8 * v + e], c[8 * v + e]), __fmul_rn(p[e], s[8 * v + e]))
-                              : x[8 * v + e];
-      if (rot[v]) out[v] = narrow8(y + 8 * v);
     }
+    if (!live || h >= h1) continue;
+    float y[16];
+    uint4 out[2];
+    angles.turn(where, own[i], partner, y, out);
     if (is_q) {
-      store_bf16<DK>(a.q_out, tok, heads, h, cb, out[0], out[1]);
+      store_bf16<DK, STREAM>(a.q_out, tok, heads, h, cb, out[0], out[1]);
     } else if constexpr (KV == PKV_KV_BF16) {
-      store_bf16<DK>(a.k_pool, slot, heads, h, cb, out[0], out[1]);
+      if (is_v)
+        store_bf16<DV, STREAM>(a.v_pool, slot, heads, h, cb, out[0], out[1]);
+      else
+        store_bf16<DK, STREAM>(a.k_pool, slot, heads, h, cb, out[0], out[1]);
     } else {
-      store_coded<DK, KV>(a.k_pool, slot, heads, h, cb, y, a.k_inv);
+      store_coded<DK, KV, STREAM>(is_v ? a.v_pool : a.k_pool, slot, heads, h, cb, y, is_v ? a.v_inv : a.k_inv);
     }
   }
 }
 
 template <int DK, int DV, int KV, int ROT>
 int run_rope(RopeKvArgs& a, int n, cudaStream_t st) {
-  // one head a thread while the launch is small (latency), four once there
-  // are enough threads to fill the GPU
+  // One head a thread while the launch is small (latency), four once there are
+  // enough threads to fill the GPU (16,384 tokens of 32/8 heads of 128: 95 us
+  // with one, 79 with two or four). Past the L2's size the rows stream (same
+  // tokens: 82 us without, 86 or 83 with only loads or only stores streaming,
+  // 72 with both; below it the attention that follows finds q in the L2).
   const long long rows = (long long)n * (a.num_q_heads + 2 * a.num_kv_heads);
   const int rpt = rows * (DK / 16) >= (1 << 19) ? 4 : 1;
+  const bool stream = rows * DK * 4 > kStreamBytes;
   a.q_units = a.q ? (a.num_q_heads + rpt - 1) / rpt : 0;
   a.kv_units = (a.num_kv_heads + rpt - 1) / rpt;
   a.n_threads = (long long)n * (a.q_units + 2 * a.kv_units) * (DK / 16);
   const long long blocks = (a.n_threads + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;
-  auto kernel = rpt == 4 ? rope_kv_kernel<DK, DV, KV, ROT, 4> : rope_kv_kernel<DK, DV, KV, ROT, 1>;
+  auto kernel = rpt == 1 ? rope_kv_kernel<DK, DV, KV, ROT, 1, false>
+                : stream ? rope_kv_kernel<DK, DV, KV, ROT, 4, true>
+                         : rope_kv_kernel<DK, DV, KV, ROT, 4, false>;
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, a) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -298,7 +349,8 @@ int dispatch_rope(const pkv_config& cfg, RopeKvArgs& a, int n, cudaStream_t st) 
 }
 
 // ---------------------------------------------------------------- read-back
-// One thread reads 16 columns (block cb) of a K or V row and writes them as bf16.
+// One thread reads 8 columns of a K and of a V row and writes each as one
+// 16-byte vector, so that neighbouring threads fill whole lines.
 struct GetKvArgs {
   const void *k_pool, *v_pool;
   uint16_t *k, *v;
@@ -315,58 +367,65 @@ __global__ void __launch_bounds__(256) get_kv_kernel(GetKvArgs a) {
   pdl_wait();
   const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
   if (t >= a.n_threads) return;
-  const int cbs = a.dk / 16;
-  const long long row = t / cbs;
-  const int cb = (int)(t - row * cbs);
+  const int vecs = a.dk / 8;
+  const long long row = t / vecs;
+  const int c = (int)(t - row * vecs) * 8;  // first column
   const long long tok = row / a.heads;
   const int h = (int)(row - tok * a.heads);
   const long long slot = a.loc[tok];
   if (slot < 0 || slot >= a.num_slots) {
-    if (h == 0 && cb == 0) record_error(a.plan, PKV_DEV_BAD_SLOT, (int)tok);
+    if (h == 0 && c == 0) record_error(a.plan, PKV_DEV_BAD_SLOT, (int)tok);
     return;
+  }
+  // both rows' codes first
+  uint4 x[2];
+  uint32_t scale8[2] = {0, 0};
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const int d = which ? a.dv : a.dk;
+    if (c >= d) continue;
+    const uint8_t* pool = static_cast<const uint8_t*>(which ? a.v_pool : a.k_pool);
+    if constexpr (KV == PKV_KV_BF16) {
+      x[which] = *reinterpret_cast<const uint4*>(pool + ((slot * a.heads + h) * d + c) * 2);
+    } else if constexpr (KV == PKV_KV_FP8_E4M3) {
+      const uint2 y = *reinterpret_cast<const uint2*>(pool + (slot * a.heads + h) * d + c);
+      x[which].x = y.x, x[which].y = y.y;
+    } else {
+      const uint8_t* tile = pool + ((slot / kSegSlots) * a.heads + h) * fp4_tile_bytes(d);
+      const int r = (int)(slot % kSegSlots);
+      x[which].x = *reinterpret_cast<const uint32_t*>(tile + r * (d / 2) + c / 2);
+      scale8[which] = tile[kSegSlots * (d / 2) + r * (d / 16) + c / 16];
+    }
   }
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     const int d = which ? a.dv : a.dk;
-    if (cb * 16 >= d) continue;
-    const uint8_t* pool = static_cast<const uint8_t*>(which ? a.v_pool : a.k_pool);
+    if (c >= d) continue;
     const float scale = which ? a.v_scale : a.k_scale;
-    uint4* dst = reinterpret_cast<uint4*>((which ? a.v : a.k) + (tok * a.heads + h) * d + cb * 16);
+    uint4* dst = reinterpret_cast<uint4*>((which ? a.v : a.k) + (tok * a.heads + h) * d + c);
     if constexpr (KV == PKV_KV_BF16) {
-      const uint4* src = reinterpret_cast<const uint4*>(pool + ((slot * a.heads + h) * d + cb * 16) * 2);
-      const uint4 x0 = src[0], x1 = src[1];
-      dst[0] = x0;
-      dst[1] = x1;
+      *dst = x[which];
     } else {
-      uint32_t w[8];  // 16 values as f16 pairs, exact
+      uint32_t w[4];  // 8 values as f16 pairs, exact
       if constexpr (KV == PKV_KV_FP8_E4M3) {
-        const uint4 x = *reinterpret_cast<const uint4*>(pool + (slot * a.heads + h) * d + cb * 16);
-        const uint32_t c[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[2 * i] = e4m3x2_to_f16x2((uint16_t)(c[i] & 0xffffu));
-          w[2 * i + 1] = e4m3x2_to_f16x2((uint16_t)(c[i] >> 16));
-        }
+        w[0] = e4m3x2_to_f16x2((uint16_t)(x[which].x & 0xffffu));
+        w[1] = e4m3x2_to_f16x2((uint16_t)(x[which].x >> 16));
+        w[2] = e4m3x2_to_f16x2((uint16_t)(x[which].y & 0xffffu));
+        w[3] = e4m3x2_to_f16x2((uint16_t)(x[which].y >> 16));
       } else {
-        const uint8_t* tile = pool + ((slot / kSegSlots) * a.heads + h) * fp4_tile_bytes(d);
-        const int r = (int)(slot % kSegSlots);
-        const uint2 x = *reinterpret_cast<const uint2*>(tile + r * (d / 2) + cb * 8);
-        const uint32_t s8 = tile[kSegSlots * (d / 2) + r * (d / 16) + cb];
-        const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(s8 | (s8 << 8)));
-        e2m1x8_to_f16x2(x.x, w);
-        e2m1x8_to_f16x2(x.y, w + 4);
+        const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(scale8[which] | (scale8[which] << 8)));
+        e2m1x8_to_f16x2(x[which].x, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = mul_f16x2(w[i], s2);  // exact: at most 6 significant bits
+        for (int i = 0; i < 4; ++i) w[i] = mul_f16x2(w[i], s2);  // exact: at most 6 significant bits
       }
-      uint32_t o[8];
+      uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const float lo = __half2float(__ushort_as_half((unsigned short)(w[i] & 0xffffu)));
         const float hi = __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
         o[i] = pack_bf16(__fmul_rn(lo, scale), __fmul_rn(hi, scale));
       }
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      *dst = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -415,7 +474,7 @@ int launch_get_kv_buffer(Ctx& c, const void* k_pool, const void* v_pool, const i
   a.heads = c.cfg.num_kv_heads;
   a.dk = c.cfg.head_dim;  // the K heads are at least as wide as the V heads (check_config)
   a.dv = head_dim_v(c.cfg);
-  a.n_threads = (long long)n * a.heads * (a.dk / 16);
+  a.n_threads = (long long)n * a.heads * (a.dk / 8);
   a.num_slots = (long long)c.cfg.num_pages * c.cfg.page_size;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
