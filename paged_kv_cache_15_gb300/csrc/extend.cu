@@ -1111,6 +1111,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) extend_tc_kernel(const __grid_
       // l: the row's running sum of p
       float m_ref = 0.f, l = 0.f;
       bool aborted = false;
+      // with a distance bias the reference starts at the bias of the first
+      // tile's nearest (or, slope negative, farthest) key, so that a split far
+      // from its rows does not begin by moving it
+      if constexpr (EXTRAS == kExtrasBias) {
+        const int first = ukv.tile(x, 0) * kExtendKeys;
+        m_ref = fmaxf(slope * (float)min(first + kExtendKeys - 1 - limit, 0), slope * (float)min(first - limit, 0));
+      }
       // the form of the scores: the polynomial until a key leaves its range
       const int far_form = a.mods.cap2 > kQuotientCap2 ? kEither : kQuotient;
       int how = a.mods.cap2 == 0.f ? kLinear : kPoly;

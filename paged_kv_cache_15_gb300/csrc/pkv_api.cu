@@ -86,7 +86,9 @@ Layout make_layout(const pkv_config& cfg, int num_sms, size_t part_bytes = sizeo
   int dctas, ectas;
   grid_sizes(cfg, num_sms, &dctas, &ectas);
   const int group = cfg.num_q_heads / cfg.num_kv_heads;
-  const long long target = (long long)dctas * kDecodeTargetWaves;
+  // (never below the plan's aim, decode_target_waves)
+  const long long target =
+      (long long)dctas * (cfg.kv_dtype == PKV_KV_FP4_E2M1 ? kDecodeTargetWavesFp4 : kDecodeTargetWaves);
   L.max_decode_items = (int)(target + cfg.max_batch + 1);
   // unsplit units, plus the splits of requests whose rows fit one unit
   L.max_extend_tiles = (int)(((long long)cfg.max_q_tokens * group + kExtendUnitRows - 1) / kExtendUnitRows +

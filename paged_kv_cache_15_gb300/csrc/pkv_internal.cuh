@@ -33,7 +33,11 @@ constexpr int kPageSizeLarge = 128;
 // 128 rows each and pay more per unit
 constexpr int kDecodeTargetWaves = 8;
 constexpr int kVerifyTargetWaves = 4;
+// 4-bit units bring 3.6 times fewer bytes a key, so their fixed cost weighs more
+// and fewer, longer ones do better (8 requests of 32K-131K keys: 160 us at 4
+// rounds, 168 at 8 and 175 at 6; 64 of 1K-8K: 79, 82, 79)
 constexpr int kDecodeTargetWavesFp4 = 4;
+static_assert(kDecodeTargetWavesFp4 >= kVerifyTargetWaves, "the layout's bound on items covers the verify plan");
 // decode splits of one request at most: the merge reads two per lane (so at
 // most 64); a lone long request then still spreads over the whole grid
 constexpr int kMaxSplitsPerRequest = 64;
