@@ -75,9 +75,9 @@ def work_of(W):
     Q in, O out, LSE out, page indices. flops: 2 * (D + Dv) per (query row,
     visible key) pair (QK^T over the K width and PV over the V width, as
     multiply-adds); D = Dv = head_dim unless K and V heads differ in width."""
-    esz = 1 if W.is_fp8 else 2
+    esz = W.elem_bytes
     L = W.seq_lens.astype(np.int64)
-    kv_bytes = int(L.sum()) * W.num_kv_heads * (W.head_dim + W.dv) * esz
+    kv_bytes = int(int(L.sum()) * W.num_kv_heads * (W.head_dim + W.dv) * esz)
     T = W.total_q
     io_bytes = T * W.num_q_heads * (W.head_dim + W.dv) * 2 + T * W.num_q_heads * 4
     idx_bytes = int(((L + W.page_size - 1) // W.page_size).sum()) * 4
@@ -180,14 +180,18 @@ def oracle_sample(W, budget_s=15.0):
     import oracle
     from tests._pipeline import oracle_pools
     from paged_kv_cache_15_gb300.workloads import bf16_bits
-    kp, vp = oracle_pools(W)
+    if W.is_fp4:  # the oracle reads 4-bit pools as decoded values
+        from tests._operators import pool_values, pools_after_append
+        kp, vp = (pool_values(W, p, d) for p, d in zip(pools_after_append(W), (W.head_dim, W.dv)))
+    else:
+        kp, vp = oracle_pools(W)
     meta = oracle.build_metadata(W.seq_lens, W.page_table, W.page_size,
                                  qo_lens=None if W.mode == "decode" else W.qo_lens)
     qo_indptr = meta["qo_indptr"]
     qbits = bf16_bits(W.q)
     nthreads = os.cpu_count() or 1
-    kv = oracle.KV_FP8_E4M3 if W.is_fp8 else oracle.KV_BF16
-    esz = 1 if W.is_fp8 else 2
+    kv = oracle.KV_F64 if W.is_fp4 else oracle.KV_FP8_E4M3 if W.is_fp8 else oracle.KV_BF16
+    esz = W.elem_bytes
     block = 8 if W.mode == "extend" else 1 << 30  # tokens per oracle call
     done_kv = done_pairs = done_tok = 0
     reqs = set()
@@ -295,7 +299,7 @@ def roofline_of(W, work, fwd_s, spec, B):
     name = W.name if W.mode != "verify" else f"{W.name}/{'prefill' if on_extend else 'decode'}_path"
     tr = NCU_TRAFFIC.get((key, name))
     roof["traffic"] = None
-    if tr and tr["src_sha"] == src_sha("extend.cu" if on_tc else "decode.cu"):
+    if tr and not W.is_fp4 and tr["src_sha"] == src_sha("extend.cu" if on_tc else "decode.cu"):
         roof["traffic"] = tr["bytes_per_launch"]
     roof["kernel"] = key
     roof["timed"] = ("forward call (attention kernel plus the split merge kernel), CUDA events on the "
@@ -546,7 +550,7 @@ def run_ours(args, W, rank, world, local):
         cpu, _ = oracle_sample(W, budget_s=args.ref_budget)
     line = {"metric": METRIC, "value": value, "unit": unit, "n_gpus": world, "steps": args.steps,
             "warmup": args.warmup, "ms_per_step": step_s * 1e3, "higher_is_better": True, "scaling": "weak",
-            "vs_baseline": None, "dtype": "fp8_e4m3 kv / bf16 q" if W.is_fp8 else "bf16",
+            "vs_baseline": None, "dtype": f"{W.kv_dtype} kv / bf16 q" if W.kv_dtype != "bf16" else "bf16",
             "data": "synthetic",
             "config": config_of(W, args.spec_mode, world),
             "us_per_call": fwd_s * 1e6,
@@ -576,7 +580,7 @@ def main():
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--spec-mode", default="prefill", choices=["prefill", "decode"])
     ap.add_argument("--page-size", type=int, default=16, choices=[16, 128])
-    ap.add_argument("--kv-dtype", default=None, choices=["bf16", "fp8_e4m3"],
+    ap.add_argument("--kv-dtype", default=None, choices=["bf16", "fp8_e4m3", "fp4_e2m1"],
                     help="pool element type (default: the workload's own)")
     ap.add_argument("--head-dims", type=int, nargs=2, default=None, metavar=("DK", "DV"),
                     help="widths of the Q/K and V heads (default: the workload's own)")

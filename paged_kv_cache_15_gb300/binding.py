@@ -224,11 +224,11 @@ def pkv_rope_set_kv_buffer(ctx, k_pool, v_pool, loc, positions, cos_sin, q, k, v
     position's angles and then their sines; q_out: contiguous (q and q_out None: k and v alone)."""
     if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
         raise ValueError("cos_sin: expected fp32 [max_positions, rotary_dim]")
-    n = len(loc)
-    if len(positions) != n or len(k) != n or len(v) != n:
+    n = loc.shape[0]
+    if positions.shape[0] != n or k.shape[0] != n or v.shape[0] != n:
         raise ValueError("loc, positions, k and v hold different numbers of tokens")
     if q is not None or q_out is not None:
-        if q is None or q_out is None or q_out.shape != q.shape or q_out.dtype != q.dtype or len(q) != n:
+        if q is None or q_out is None or q_out.shape != q.shape or q_out.dtype != q.dtype or q.shape[0] != n:
             raise ValueError("q_out: expected a tensor like q, and q loc's number of tokens")
     rope = pkv_rope(_ptr(cos_sin), *cos_sin.shape, rotary_offset, 1 if interleaved else 0)
     (qp, qs), (kp, ks), (vp_, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
@@ -239,8 +239,8 @@ def pkv_rope_set_kv_buffer(ctx, k_pool, v_pool, loc, positions, cos_sin, q, k, v
 
 def pkv_get_kv_buffer(ctx, k_pool, v_pool, loc, k, v, k_scale=1.0, v_scale=1.0, stream=None) -> None:
     """Rows of the pools at slots loc, as bf16, into k and v ([tokens, num_kv_heads, width], contiguous)."""
-    n = len(loc)
-    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or len(k) != n or len(v) != n:
+    n = loc.shape[0]
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.shape[0] != n or v.shape[0] != n:
         raise ValueError("k and v: expected bf16 with loc's number of tokens")
     _check(lib().pkv_get_kv_buffer(ctx, _ptr(k_pool), _ptr(v_pool), _int32(loc, "loc"), _ptr(k), _ptr(v), n,
                                    float(k_scale), float(v_scale), _stream(stream)), "pkv_get_kv_buffer")

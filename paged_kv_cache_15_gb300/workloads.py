@@ -115,6 +115,11 @@ class Workload:
     def is_fp4(self) -> bool:
         return self.kv_dtype == "fp4_e2m1"
 
+    @property
+    def elem_bytes(self) -> float:
+        """Bytes a pool element takes (4-bit codes with their share of the block scales)."""
+        return {"bf16": 2, "fp8_e4m3": 1, "fp4_e2m1": 0.5625}[self.kv_dtype]
+
 
 def fp4_pack_rows(values: torch.Tensor, inv_scale: float):
     """fp32 rows [n, heads, D] -> (codes [n, heads, D], scale bytes [n, heads, D/16]): E2M1 codes (nearest, ties to the
