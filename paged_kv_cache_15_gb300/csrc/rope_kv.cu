@@ -13,13 +13,13 @@
 // Bound by memory: q, k and v are read once, q_out and the pool rows written
 // once. One thread owns 16 columns of a head (a whole 4-bit block, 32 bytes of
 // bf16) and runs over RPT heads of its token with the angles of those columns
-// in registers. 16,384 tokens of 32/8 heads of 128 into bf16 pools: 72.4 us,
-// 5,680 GB/s or 0.84 of the copy rate; 64 tokens into E4M3 pools: 2.1 us, the
-// launch and the chain of slot, angles and rows. Tried and not kept: a
-// persistent grid that takes a token a stage through a shared-memory ring by
-// bulk copies (73 us, and slower than this below 8,000 tokens); more threads an
-// SM (82, 89 and 113 us at 6, 8 and 10 blocks: the DRAM pages, not latency,
-// limit the large pass).
+// in registers. 16,384 tokens of 32/8 heads of 128 into bf16 pools: 76.7 us on
+// inputs that change from pass to pass, 5,360 GB/s or 0.79 of the copy rate;
+// 64 tokens into E4M3 pools: 2.1 us, the launch and the chain of slot, angles
+// and rows. Tried and not kept: a persistent grid that takes a token a stage
+// through a shared-memory ring by bulk copies (7 % faster at 16,384 tokens than
+// this kernel without streaming, slower below 8,000); more threads an SM (82,
+// 89 and 113 us at 6, 8 and 10 blocks, where 82 was the default's).
 #include <cmath>
 
 #include "pkv_internal.cuh"
@@ -325,8 +325,9 @@ int run_rope(RopeKvArgs& a, int n, cudaStream_t st) {
   // One head a thread while the launch is small (latency), four once there are
   // enough threads to fill the GPU (16,384 tokens of 32/8 heads of 128: 95 us
   // with one, 79 with two or four). Past the L2's size the rows stream (same
-  // tokens: 82 us without, 86 or 83 with only loads or only stores streaming,
-  // 72 with both; below it the attention that follows finds q in the L2).
+  // tokens, inputs that change: 81.9 us without, 76.7 with loads and stores
+  // streaming, neither alone gains; below it the attention that follows finds q
+  // in the L2).
   const long long rows = (long long)n * (a.num_q_heads + 2 * a.num_kv_heads);
   const int rpt = rows * (DK / 16) >= (1 << 19) ? 4 : 1;
   const bool stream = rows * DK * 4 > kStreamBytes;
