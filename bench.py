@@ -44,12 +44,12 @@ FALLBACK_BF16_TFLOPS = 1900.0
 # workload (dram__bytes_read.sum + dram__bytes_write.sum), valid only while the
 # kernel's source file is unchanged (src_sha: first 16 hex digits of its sha256).
 NCU_TRAFFIC = {
-    ("decode_splitkv", "llama3_8b_decode"): {"src_sha": "8e2560c6c19b5067", "bytes_per_launch": 1386290688},
-    ("decode_splitkv", "long_fp8_decode"): {"src_sha": "8e2560c6c19b5067", "bytes_per_launch": 1471689728},
-    ("extend_tc", "prefix_extend"): {"src_sha": "a645927089a35229", "bytes_per_launch": 271852032},
-    ("extend_tc", "prefix_extend_fp8"): {"src_sha": "a645927089a35229", "bytes_per_launch": 193205760},
-    ("extend_tc", "spec_verify/decode_path"): {"src_sha": "a645927089a35229", "bytes_per_launch": 599808000},
-    ("extend_tc", "spec_verify/prefill_path"): {"src_sha": "a645927089a35229", "bytes_per_launch": 599735296},
+    ("decode_splitkv", "llama3_8b_decode"): {"src_sha": "d1c84212b85caf54", "bytes_per_launch": 1386052352},
+    ("decode_splitkv", "long_fp8_decode"): {"src_sha": "d1c84212b85caf54", "bytes_per_launch": 1471586304},
+    ("extend_tc", "prefix_extend"): {"src_sha": "b97d50961ec3a706", "bytes_per_launch": 272068608},
+    ("extend_tc", "prefix_extend_fp8"): {"src_sha": "b97d50961ec3a706", "bytes_per_launch": 192848128},
+    ("extend_tc", "spec_verify/decode_path"): {"src_sha": "b97d50961ec3a706", "bytes_per_launch": 599944448},
+    ("extend_tc", "spec_verify/prefill_path"): {"src_sha": "b97d50961ec3a706", "bytes_per_launch": 599618304},
 }
 
 

@@ -56,7 +56,7 @@ DECODE = {
     "g3": (6, 2, [1, 900, 450, 129]),
     "g4": (32, 8, [1023, 2, 511, 4000, 640]),
     "g8": (32, 4, [640, 63, 1500]),
-    "g12": (24, 2, [700, 31, 2049]),
+    "g12": (36, 3, [700, 31, 2049]),
     "g16": (32, 2, [129, 2500, 16]),
     "long": (8, 1, [40000, 7]),
 }
